@@ -65,7 +65,8 @@ typedef enum {
     CONVROT_ERR_UNSUPPORTED = 8,     /* device is not sm_100 */
     CONVROT_ERR_SCRATCH_LIMIT = 9,   /* needs more than the built-in scratch array */
     CONVROT_ERR_NOT_DEVICE = 10,     /* a pointer is not memory of the current device */
-    CONVROT_ERR_OVERLAP = 11         /* input and output buffers overlap */
+    CONVROT_ERR_OVERLAP = 11,        /* input and output buffers overlap */
+    CONVROT_ERR_PAGE = 12            /* a slot or page id outside the cache (convrot_kv4.h) */
 } convrot_status;
 
 /* Human-readable name of a status (static storage, never NULL).  The pages

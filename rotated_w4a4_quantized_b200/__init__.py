@@ -14,12 +14,19 @@ the W4A16 variant (``include/convrot_w4a16.h``, library
 ``convrot_w4a16_linear`` and ``convrot_w4a16_linear_prepared``, and for the
 NVFP4 variant (``include/convrot_nvfp4.h``, library ``libconvrot_nvfp4.so``)
 ``convrot_nvfp4_quantize``, ``convrot_nvfp4_linear`` and
-``convrot_nvfp4_linear_prepared``.
+``convrot_nvfp4_linear_prepared``.  For generating tokens there are the
+group-scaled few-token layer (``include/convrot_w4g.h``, library
+``libconvrot_w4g.so``): ``convrot_w4g_quantize_weight`` and
+``convrot_w4g_linear``; and the INT4 cache of keys and values
+(``include/convrot_kv4.h``, library ``libconvrot_kv4.so``):
+``convrot_kv4_new_cache``, ``convrot_kv4_plan``, ``convrot_kv4_append``,
+``convrot_kv4_read`` and ``convrot_kv4_attention``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -27,12 +34,15 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 LIB_W4A16_PATH = os.path.join(_HERE, "libconvrot_w4a16.so")
 LIB_NVFP4_PATH = os.path.join(_HERE, "libconvrot_nvfp4.so")
+LIB_W4G_PATH = os.path.join(_HERE, "libconvrot_w4g.so")
+LIB_KV4_PATH = os.path.join(_HERE, "libconvrot_kv4.so")
 
 STATUS = {
     0: "CONVROT_OK", 1: "CONVROT_ERR_NULL", 2: "CONVROT_ERR_GROUP", 3: "CONVROT_ERR_SHAPE",
     4: "CONVROT_ERR_ALIGN", 5: "CONVROT_ERR_WORKSPACE", 6: "CONVROT_ERR_CUDA",
     7: "CONVROT_ERR_DEVICE_TIMEOUT", 8: "CONVROT_ERR_UNSUPPORTED", 9: "CONVROT_ERR_SCRATCH_LIMIT",
     10: "CONVROT_ERR_NOT_DEVICE", 11: "CONVROT_ERR_OVERLAP",
+    12: "CONVROT_ERR_PAGE",
 }
 MAX_K = 32768
 
@@ -871,3 +881,333 @@ def convrot_debug_gemm_plan(M: int, N: int, K: int, pairs: int = 74, sms: int = 
                                          ctypes.byref(st), ctypes.byref(sp)),
            "convrot_debug_gemm_plan")
     return t.value, st.value, sp.value
+
+
+# ---------------------------------------------------------------------------
+# the group-scaled few-token layer (include/convrot_w4g.h)
+# ---------------------------------------------------------------------------
+
+def _load(path: str, sigs: dict) -> ctypes.CDLL:
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"{path} is missing: build it with `python -m rotated_w4a4_quantized_b200.build` "
+            "(there is no fallback path)")
+    L = ctypes.CDLL(path)
+    for name, (args, res) in sigs.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = res
+    return L
+
+
+class _On:
+    """The operands' device as the current one; nothing to do where it is."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, t: torch.Tensor):
+        self.index = t.device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _raw_stream(index: int, stream):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _keep(t: torch.Tensor, stream):
+    """A workspace of this call's own: its memory is not reused before the
+    work on `stream` is done, where that is not the current stream."""
+    if stream is not None:
+        t.record_stream(stream)
+
+
+_lib_w4g = None
+
+
+def lib_w4g() -> ctypes.CDLL:
+    """The loaded group-scaled library; raises if it has not been built."""
+    global _lib_w4g
+    if _lib_w4g is None:
+        P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        _lib_w4g = _load(LIB_W4G_PATH, {
+            "convrot_w4g_quantize_weight": ([P, I64, I64, I, I, P, P, P], I),
+            "convrot_w4g_workspace_size": ([I64, I64, I], SZ),
+            "convrot_w4g_linear": ([P, P, P, P, I64, I64, I64, I, I, P, SZ, P, P], I),
+        })
+    return _lib_w4g
+
+
+def convrot_w4g_quantize_weight(w, group: int, scale_group: int, qw=None, sg=None, stream=None):
+    """bf16 [N, K] -> (packed codes uint8 [N, K/2], bf16 scales
+    [N, K/scale_group]).  group 64 or 256 rotates the rows first, 0 takes them
+    as they are; scale_group is 32, 64 or 128."""
+    N, K = _rows(w, torch.bfloat16, "w")
+    if scale_group not in (32, 64, 128):
+        raise ConvRotError(2, "convrot_w4g_quantize_weight")
+    with _On(w):
+        qw = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device) if qw is None else qw
+        sg = torch.empty(N, K // scale_group, dtype=torch.bfloat16, device=w.device) if sg is None else sg
+        _need(qw, torch.uint8, "qw", (N, K // 2), w)
+        _need(sg, torch.bfloat16, "sg", (N, K // scale_group), w)
+        _check(lib_w4g().convrot_w4g_quantize_weight(
+            w.data_ptr(), N, K, group, scale_group, qw.data_ptr(), sg.data_ptr(),
+            _raw_stream(w.device.index, stream)), "convrot_w4g_quantize_weight")
+    return qw, sg
+
+
+def convrot_w4g_workspace_size(M: int, K: int, group: int) -> int:
+    return int(lib_w4g().convrot_w4g_workspace_size(M, K, group))
+
+
+def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=None, out=None,
+                       stream=None):
+    """The whole group-scaled layer: bf16 x [M, K] -> bf16 y [M, N], with the
+    weights of convrot_w4g_quantize_weight (the same group and scale_group).
+    group 0 takes x as it is: rotated already, or with weights that are not.
+    Made for few tokens: every 16 of them read the weights once."""
+    M, K = _rows(x, torch.bfloat16, "x")
+    if scale_group not in (32, 64, 128):
+        raise ConvRotError(2, "convrot_w4g_linear")
+    _need(qw, torch.uint8, "qw", (None, K // 2), x)
+    N = qw.shape[0]
+    _need(sg, torch.bfloat16, "sg", (N, K // scale_group), x)
+    _need_opt(bias, torch.bfloat16, "bias", (N,), x)
+    L = lib_w4g()
+    with _On(x):
+        need = L.convrot_w4g_workspace_size(M, K, group)
+        if workspace is not None:
+            _need(workspace, torch.uint8, "workspace", None, x)
+            if workspace.numel() < need:
+                raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} needed")
+        elif need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            _keep(workspace, stream)
+        if out is None:
+            out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        else:
+            _need(out, torch.bfloat16, "out", (M, N), x)
+        _check(L.convrot_w4g_linear(
+            x.data_ptr(), qw.data_ptr(), sg.data_ptr(), None if bias is None else bias.data_ptr(),
+            M, N, K, group, scale_group, None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), out.data_ptr(),
+            _raw_stream(x.device.index, stream)), "convrot_w4g_linear")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the INT4 cache of keys and values (include/convrot_kv4.h)
+# ---------------------------------------------------------------------------
+
+class _Kv4CacheArg(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int), ("page", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("group", ctypes.c_int)]
+
+
+class Kv4Cache(NamedTuple):
+    """A paged cache: codes uint8 [pages, kv_heads, page, D/2] and scales bf16
+    [pages, kv_heads, page], of the keys and of the values."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+_lib_kv4 = None
+
+
+def lib_kv4() -> ctypes.CDLL:
+    """The loaded cache library; raises if it has not been built."""
+    global _lib_kv4
+    if _lib_kv4 is None:
+        P, I64, I, SZ, F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
+                            ctypes.c_float)
+        C = ctypes.POINTER(_Kv4CacheArg)
+        _lib_kv4 = _load(LIB_KV4_PATH, {
+            "convrot_kv4_plan": ([P, P, I64, I, P, I64, P, I64, P, I64, P, P, P, P, P, P], I),
+            "convrot_kv4_append": ([C, P, I64, P, I64, P, I64, P], I),
+            "convrot_kv4_read": ([C, P, I64, P, P, P], I),
+            "convrot_kv4_attention_workspace_size": ([I64, I64, I, I, I, I64], SZ),
+            "convrot_kv4_attention": ([C, P, I64, I64, I, P, I64, P, P, I64, F, P, SZ, P, P], I),
+            "convrot_kv4_check_device_error": ([P], I),
+        })
+    return _lib_kv4
+
+
+def convrot_kv4_new_cache(num_pages: int, kv_heads: int, page: int, head_dim: int, device) -> Kv4Cache:
+    """An empty cache of num_pages pages of `page` tokens."""
+    def codes():
+        return torch.zeros(num_pages, kv_heads, page, head_dim // 2, dtype=torch.uint8, device=device)
+
+    def scales():
+        return torch.zeros(num_pages, kv_heads, page, dtype=torch.bfloat16, device=device)
+    return Kv4Cache(codes(), scales(), codes(), scales())
+
+
+def _kv4_cache(cache, group: int) -> _Kv4CacheArg:
+    kc, ks, vc, vs = cache
+    _need(kc, torch.uint8, "k_codes", (None, None, None, None))
+    shape = kc.shape
+    _need(ks, torch.bfloat16, "k_scales", shape[:3], kc)
+    _need(vc, torch.uint8, "v_codes", shape, kc)
+    _need(vs, torch.bfloat16, "v_scales", shape[:3], kc)
+    return _Kv4CacheArg(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1],
+                        shape[2], 2 * shape[3], group)
+
+
+def _need_tokens(t, name: str, heads, head_dim: int, like) -> int:
+    """bf16 [T, heads, head_dim], dense within a token; returns the values
+    between tokens (columns of a fused projection's rows qualify)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
+    if (not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != head_dim
+            or (heads is not None and t.shape[1] != heads)):
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor [tokens, "
+                         f"{'heads' if heads is None else heads}, {head_dim}] "
+                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {like.device}")
+    T, H, _ = t.shape
+    st, sh, sd = t.stride()
+    if T == 0 or H == 0:
+        return H * head_dim
+    if sd != 1 or (H > 1 and sh != head_dim) or (T > 1 and st < H * head_dim):
+        raise ValueError(f"{name} must be dense within a token (strides {t.stride()})")
+    return st if T > 1 else H * head_dim
+
+
+class Kv4Plan:
+    """What convrot_kv4_plan lays out: seq_lens int32 [B], cu_q int32 [B + 1],
+    slots int64 [max_tokens], positions int32 [max_tokens] and result int32 [4]
+    = {free pages left, pages taken, new tokens, status}."""
+    __slots__ = ("seq_lens", "cu_q", "slots", "positions", "result")
+
+    def __init__(self, seq_lens, cu_q, slots, positions, result):
+        self.seq_lens, self.cu_q, self.slots = seq_lens, cu_q, slots
+        self.positions, self.result = positions, result
+
+    @property
+    def free_count(self):
+        """int32 [1]: free pages left, the next step's free_count."""
+        return self.result[:1]
+
+    @property
+    def status(self):
+        """int32 [1]: 0 when the step was laid out (include/convrot_kv4.h)."""
+        return self.result[3:]
+
+
+def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, page: int,
+                     max_tokens: int, stream=None) -> Kv4Plan:
+    """The bookkeeping of one step on the GPU: cached and new_tokens int32 [B]
+    (-1 new tokens: finished, its pages go back), block_table int32
+    [B, max_pages] (completed in place), free_pages int32 [capacity] (a stack of
+    free_count int32 [1] page ids; returned pages are pushed in place)."""
+    _need(cached, torch.int32, "cached", (None,))
+    B = cached.shape[0]
+    _need(new_tokens, torch.int32, "new_tokens", (B,), cached)
+    _need(block_table, torch.int32, "block_table", (B, None), cached)
+    _need(free_pages, torch.int32, "free_pages", (None,), cached)
+    _need(free_count, torch.int32, "free_count", (1,), cached)
+    if max_tokens < 0:
+        raise ValueError("max_tokens is negative")
+    with _On(cached):
+        dev = cached.device
+        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        result = torch.empty(4, dtype=torch.int32, device=dev)
+        _check(lib_kv4().convrot_kv4_plan(
+            cached.data_ptr(), new_tokens.data_ptr(), B, page, block_table.data_ptr(),
+            block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(),
+            max_tokens, seq_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+            result.data_ptr(), _raw_stream(dev.index, stream)), "convrot_kv4_plan")
+    return Kv4Plan(seq_lens, cu_q, slots, positions, result)
+
+
+def convrot_kv4_append(k, v, cache, slots, group: int, stream=None) -> None:
+    """Quantise keys and values, bf16 [T, kv_heads, D], into the cache at
+    slots int64 [T] (negative: skipped)."""
+    c = _kv4_cache(cache, group)
+    kc = cache[0]
+    ldk = _need_tokens(k, "k", c.kv_heads, c.head_dim, kc)
+    ldv = _need_tokens(v, "v", c.kv_heads, c.head_dim, kc)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
+    _need(slots, torch.int64, "slots", (T,), kc)
+    with _On(kc):
+        _check(lib_kv4().convrot_kv4_append(c, k.data_ptr(), ldk, v.data_ptr(), ldv, slots.data_ptr(), T,
+                                            _raw_stream(kc.device.index, stream)), "convrot_kv4_append")
+
+
+def convrot_kv4_read(cache, slots, group: int, k=None, v=None, stream=None):
+    """The cached rows of slots int64 [T], rotated back: (k, v) bf16
+    [T, kv_heads, D]; zeros where the slot is negative."""
+    c = _kv4_cache(cache, group)
+    kc = cache[0]
+    _need(slots, torch.int64, "slots", (None,), kc)
+    shape = (slots.shape[0], c.kv_heads, c.head_dim)
+    with _On(kc):
+        k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if k is None else _need(k, torch.bfloat16, "k", shape, kc)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if v is None else _need(v, torch.bfloat16, "v", shape, kc)
+        _check(lib_kv4().convrot_kv4_read(c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+                                          _raw_stream(kc.device.index, stream)), "convrot_kv4_read")
+    return k, v
+
+
+def convrot_kv4_attention_workspace_size(T: int, B: int, heads: int, kv_heads: int, head_dim: int,
+                                         max_keys: int) -> int:
+    return int(lib_kv4().convrot_kv4_attention_workspace_size(T, B, heads, kv_heads, head_dim, max_keys))
+
+
+def convrot_kv4_attention(q, cache, block_table, seq_lens, cu_q, scale: float, group: int,
+                          workspace=None, out=None, stream=None):
+    """Attention of the newest tokens over the cache: q bf16 [T, heads, D] ->
+    bf16 [T, heads, D].  Request b's queries are tokens cu_q[b] .. cu_q[b + 1]
+    - 1, the last of its seq_lens[b] tokens, whose rows are in the cache; its
+    pages are listed in block_table[b].  Without `out`, rows behind the last
+    request are whatever the new tensor held."""
+    c = _kv4_cache(cache, group)
+    kc = cache[0]
+    ldq = _need_tokens(q, "q", None, c.head_dim, kc)
+    T, heads, D = q.shape
+    _need(seq_lens, torch.int32, "seq_lens", (None,), kc)
+    B = seq_lens.shape[0]
+    _need(block_table, torch.int32, "block_table", (B, None), kc)
+    _need(cu_q, torch.int32, "cu_q", (B + 1,), kc)
+    L = lib_kv4()
+    with _On(kc):
+        need = L.convrot_kv4_attention_workspace_size(T, B, heads, c.kv_heads, D,
+                                                      block_table.shape[1] * c.page)
+        if workspace is None:
+            workspace = torch.empty(max(1, need), dtype=torch.uint8, device=kc.device)
+            _keep(workspace, stream)
+        else:
+            _need(workspace, torch.uint8, "workspace", None, kc)
+            if workspace.numel() < need:
+                raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} needed")
+        if out is None:
+            out = torch.empty(T, heads, D, dtype=torch.bfloat16, device=kc.device)
+        else:
+            _need(out, torch.bfloat16, "out", (T, heads, D), kc)
+        _check(L.convrot_kv4_attention(
+            c, q.data_ptr(), ldq, T, heads, block_table.data_ptr(), block_table.shape[1],
+            seq_lens.data_ptr(), cu_q.data_ptr(), B, scale, workspace.data_ptr(), workspace.numel(),
+            out.data_ptr(), _raw_stream(kc.device.index, stream)), "convrot_kv4_attention")
+    return out
+
+
+def convrot_kv4_check_device_error(stream=None) -> int:
+    """Synchronise the stream; return (and clear) the cache library's device
+    error status (12: a slot or page id outside the cache was met)."""
+    return int(lib_kv4().convrot_kv4_check_device_error(_stream(stream)))

@@ -1,12 +1,14 @@
 """Build the CUDA libraries in-tree: rotated_w4a4_quantized_b200/libconvrot.so
 (the W4A4 layer, include/convrot.h), libconvrot_w4a16.so (the W4A16
-variant, include/convrot_w4a16.h) and libconvrot_nvfp4.so (the NVFP4
-variant, include/convrot_nvfp4.h).
+variant, include/convrot_w4a16.h), libconvrot_nvfp4.so (the NVFP4
+variant, include/convrot_nvfp4.h), libconvrot_w4g.so (the group-scaled
+few-token variant, include/convrot_w4g.h) and libconvrot_kv4.so (the INT4
+cache of keys and values, include/convrot_kv4.h).
 
     python -m rotated_w4a4_quantized_b200.build [--verbose]
 
 Each library is one translation unit (csrc/convrot.cu, csrc/w4a16.cu,
-csrc/nvfp4.cu)
+csrc/nvfp4.cu, csrc/w4g.cu, csrc/kv4.cu)
 compiled for sm_100a only, with IEEE
 fp32 semantics (no fast-math: the epilogue and the quantiser rely on
 correctly rounded multiply, add and divide).  The CUDA runtime is linked
@@ -35,6 +37,13 @@ SRC_NVFP4 = os.path.join(HERE, "csrc", "nvfp4.cu")
 DEPS_NVFP4 = [os.path.join(HERE, "csrc", f) for f in ("nvfp4.cu", "prep.cuh", "ptx.cuh")] + [
     HEADER, os.path.join(_INC, "convrot_nvfp4.h")]
 LIB_NVFP4 = os.path.join(HERE, "libconvrot_nvfp4.so")
+_SHARED = [os.path.join(HERE, "csrc", f) for f in ("frag.cuh", "host.cuh", "prep.cuh", "ptx.cuh")] + [HEADER]
+SRC_W4G = os.path.join(HERE, "csrc", "w4g.cu")
+DEPS_W4G = [SRC_W4G, os.path.join(_INC, "convrot_w4g.h")] + _SHARED
+LIB_W4G = os.path.join(HERE, "libconvrot_w4g.so")
+SRC_KV4 = os.path.join(HERE, "csrc", "kv4.cu")
+DEPS_KV4 = [SRC_KV4, os.path.join(_INC, "convrot_kv4.h")] + _SHARED
+LIB_KV4 = os.path.join(HERE, "libconvrot_kv4.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -60,7 +69,8 @@ def _stale(lib: str, deps) -> bool:
 
 def stale() -> bool:
     return (_stale(LIB, DEPS + [HEADER]) or _stale(LIB_W4A16, DEPS_W4A16)
-            or _stale(LIB_NVFP4, DEPS_NVFP4))
+            or _stale(LIB_NVFP4, DEPS_NVFP4) or _stale(LIB_W4G, DEPS_W4G)
+            or _stale(LIB_KV4, DEPS_KV4))
 
 
 def _build_one(src: str, lib: str, verbose: bool) -> None:
@@ -81,6 +91,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         _build_one(SRC_W4A16, LIB_W4A16, verbose)
     if force or _stale(LIB_NVFP4, DEPS_NVFP4):
         _build_one(SRC_NVFP4, LIB_NVFP4, verbose)
+    if force or _stale(LIB_W4G, DEPS_W4G):
+        _build_one(SRC_W4G, LIB_W4G, verbose)
+    if force or _stale(LIB_KV4, DEPS_KV4):
+        _build_one(SRC_KV4, LIB_KV4, verbose)
     return LIB
 
 
@@ -89,3 +103,5 @@ if __name__ == "__main__":
     print(LIB)
     print(LIB_W4A16)
     print(LIB_NVFP4)
+    print(LIB_W4G)
+    print(LIB_KV4)

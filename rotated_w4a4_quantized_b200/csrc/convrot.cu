@@ -888,6 +888,8 @@ const char *convrot_status_string(convrot_status s) {
             return "CONVROT_ERR_NOT_DEVICE: a pointer is not memory of the current device";
         case CONVROT_ERR_OVERLAP:
             return "CONVROT_ERR_OVERLAP: input and output buffers overlap";
+        case CONVROT_ERR_PAGE:
+            return "CONVROT_ERR_PAGE: a slot or page id outside the cache was met on the device";
     }
     return "CONVROT_ERR_UNKNOWN";
 }

@@ -1,0 +1,174 @@
+// frag.cuh -- register-level pieces shared by the group-scaled linear and the
+// 4-bit cache: rotation of 16 channels a thread, exact widening of packed
+// INT4 codes to f16 / bf16 pairs, and the warp-level matrix product.
+//
+// Why mma.sync and not tcgen05 here: these kernels have 1 to 32 columns
+// (tokens or queries) and are bound by the bytes of the packed codes.  A
+// tcgen05 MMA reads its whole 128-row A operand from TMEM whatever its column
+// count, and the codes would have to be stored to TMEM first; the warp-level
+// product takes the widened codes straight from the registers they were
+// widened in.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "prep.cuh"
+
+namespace frag {
+
+// Codes of one 32-bit word (8 codes, low nibble first) as f16 pairs
+// (c0, c4), (c1, c5), (c2, c6), (c3, c7), exact.  A nibble XOR 8 is code + 8;
+// in the low mantissa bits of 0x6400 (1024.0, spacing 1) it reads
+// 1024 + code + 8, and one bit group further up 1024 + 16 (code + 8): one
+// subtraction, or one FMA with 1/16, leaves the code.
+__device__ __forceinline__ void widen_f16(uint32_t w, uint32_t (&o)[4]) {
+    const uint32_t w8 = w >> 8;
+    const __half2 lo = __halves2half2(__ushort_as_half(0xE408), __ushort_as_half(0xE408));   // -1032
+    const __half2 sc = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));   // 1 / 16
+    const __half2 hi = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));   // -72
+    uint32_t a = (w & 0x000F000Fu) ^ 0x64086408u;
+    uint32_t b = (w & 0x00F000F0u) ^ 0x64806480u;
+    uint32_t c = (w8 & 0x000F000Fu) ^ 0x64086408u;
+    uint32_t d = (w8 & 0x00F000F0u) ^ 0x64806480u;
+    __half2 ha = __hadd2(*reinterpret_cast<__half2 *>(&a), lo);
+    __half2 hb = __hfma2(*reinterpret_cast<__half2 *>(&b), sc, hi);
+    __half2 hc = __hadd2(*reinterpret_cast<__half2 *>(&c), lo);
+    __half2 hd = __hfma2(*reinterpret_cast<__half2 *>(&d), sc, hi);
+    o[0] = *reinterpret_cast<uint32_t *>(&ha);
+    o[1] = *reinterpret_cast<uint32_t *>(&hb);
+    o[2] = *reinterpret_cast<uint32_t *>(&hc);
+    o[3] = *reinterpret_cast<uint32_t *>(&hd);
+}
+
+// The same as bf16 pairs: 0x4300 is 128.0 with spacing 1, so only the low
+// nibble of each half has room and the word is shifted between pairs.
+__device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t (&o)[4]) {
+    const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xC308),
+                                                  __ushort_as_bfloat16(0xC308));             // -136
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a = ((w >> (4 * i)) & 0x000F000Fu) ^ 0x43084308u;
+        __nv_bfloat162 h = __hadd2(*reinterpret_cast<__nv_bfloat162 *>(&a), off);
+        o[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 tile of 16-bit values held one row per 4 lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float bf16_f32(uint16_t v) {
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+__device__ __forceinline__ uint16_t f32_bf16(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// ---------------------------------------------------------------- rotation
+// The unnormalised rotation of 16 consecutive channels a thread, whole groups
+// in neighbouring lanes (4 lanes for n = 64, 16 for n = 256; channel order =
+// lane order).  Digits 0 and 1 run in registers, digits 2 and 3 as shuffles;
+// every quadruple is added as (x_0 + x_1) + (x_2 + x_3), the order of the
+// prep kernels, so the bits are theirs.  All 32 lanes take part.
+__device__ __forceinline__ void lane_digit(float (&v)[16], int stride) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float pair = v[e] + __shfl_xor_sync(0xFFFFFFFFu, v[e], stride);
+        const float sum = pair + __shfl_xor_sync(0xFFFFFFFFu, pair, 2 * stride);
+        v[e] = __fmaf_rn(-2.0f, v[e], sum);
+    }
+}
+
+__device__ __forceinline__ void rotate16(float (&v)[16], bool wide) {
+    prep::radix4_digit0(v);
+    prep::radix4_stage<4>(v);
+    lane_digit(v, 1);
+    if (wide) lane_digit(v, 4);
+}
+
+// 2^-digits of the normalised matrix.
+__device__ __forceinline__ float norm_of(int group) { return group == 64 ? 0.125f : 0.0625f; }
+
+__device__ __forceinline__ void unpack_bf16x8(uint4 a, float *v) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void load16(const uint16_t *p, float (&v)[16]) {
+    unpack_bf16x8(*reinterpret_cast<const uint4 *>(p), v);
+    unpack_bf16x8(*reinterpret_cast<const uint4 *>(p + 8), v + 8);
+}
+
+__device__ __forceinline__ void store16(uint16_t *p, const float (&v)[16], float scale) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i] * scale, v[2 * i + 1] * scale);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The largest |v| over `lanes` neighbouring lanes, as float bits: an integer
+// maximum, so that an infinity or a NaN (larger still) wins.
+__device__ __forceinline__ uint32_t absmax_bits(const float (&v)[16], int lanes) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    for (int s = 1; s < lanes; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    return m;
+}
+
+// The bf16 scale of a block whose largest unnormalised |u| has the bits
+// `amax`, and the factor that takes u to q's argument.  Scales below 2^-100
+// count as 0, so that 1 / s stays finite.
+__device__ __forceinline__ uint16_t block_scale(uint32_t amax, float norm, float &factor) {
+    const uint16_t s = f32_bf16(__fdiv_rn(__uint_as_float(amax) * norm, 7.0f));
+    if (s < ((127 - 100) << 7)) {   // positive bf16 bits order like the values
+        factor = 0.0f;
+        return 0;
+    }
+    factor = __fdiv_rn(1.0f, bf16_f32(s)) * norm;
+    return s;
+}
+
+}  // namespace frag

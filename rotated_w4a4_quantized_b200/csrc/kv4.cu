@@ -1,0 +1,967 @@
+// kv4.cu -- the rotated INT4 cache of keys and values (include/convrot_kv4.h):
+// the plan of a step, append, read and the attention over the cache.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/convrot_kv4.h"
+#include "frag.cuh"
+#include "host.cuh"
+
+namespace kv4 {
+
+__device__ __forceinline__ void page_error() { atomicExch(&g_convrot_error, CONVROT_ERR_PAGE); }
+
+struct Cache {
+    uint8_t *kc;
+    uint16_t *ks;
+    uint8_t *vc;
+    uint16_t *vs;
+    int64_t num_pages;
+    int heads, page_shift, D, group;
+};
+
+// ------------------------------------------------------------------ plan
+// One pass of integer prefix sums over the requests, done by every CTA for
+// itself (B is at most 8192: three loads a thread and a block scan, a few
+// microseconds less than a second launch would cost), then a grid-stride loop
+// over the new tokens and the taken pages, each found by binary search in the
+// prefix sums in shared memory.  Nothing that one CTA writes is read by
+// another: pages that come back and go out again in the same step are read
+// from the finished request's table row, not from the stack.
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+    const int *cached, *fresh;
+    int B, page_shift;
+    int *table;
+    int64_t max_pages;
+    int *free_pages;
+    int64_t capacity;
+    const int *free_count;
+    int64_t max_tokens;
+    int *seq_lens, *cu_q;
+    long long *slots;
+    int *positions, *result;
+};
+
+// The last b of cu[0 .. B] with cu[b] <= i, among those with cu[b + 1] > i.
+__device__ __forceinline__ int find(const int *cu, int B, int i) {
+    int lo = 0, hi = B;   // cu[lo] <= i < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
+    extern __shared__ int sm[];
+    int *cu_q = sm, *cu_take = sm + (a.B + 1), *cu_back = sm + 2 * (a.B + 1);
+    __shared__ long long warp_sum[3][32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+
+    const int64_t mask = (int64_t(1) << a.page_shift) - 1;
+    long long carry[3] = {0, 0, 0};
+    for (int base = 0; base < a.B; base += kPlanThreads) {
+        const int b = base + tid;
+        long long v[3] = {0, 0, 0};
+        if (b < a.B) {
+            const int64_t c = a.cached[b], n = a.fresh[b];
+            const int64_t have = (c + mask) >> a.page_shift;
+            int why = 0;
+            if (c < 0 || have > a.max_pages) why = 4;
+            else if (n < 0) v[2] = have;
+            else {
+                const int64_t need = (c + n + mask) >> a.page_shift;
+                if (need > a.max_pages || c + n > 0x7FFFFFFF) why = 2;
+                else {
+                    v[0] = n;
+                    v[1] = need - have;
+                }
+            }
+            if (why) atomicMax(&bad, why);
+        }
+        // inclusive scan over the block
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            for (int s = 1; s < 32; s <<= 1) {
+                const long long u = __shfl_up_sync(0xFFFFFFFFu, v[k], s);
+                if (lane >= s) v[k] += u;
+            }
+            if (lane == 31) warp_sum[k][warp] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            long long before = carry[k];
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                if (w == warp) v[k] += before;
+                before += warp_sum[k][w];
+            }
+            carry[k] = before;
+        }
+        if (b < a.B) {
+            // sums beyond 2^31 - 1 are refused below, before any is used
+            cu_q[b + 1] = static_cast<int>(v[0]);
+            cu_take[b + 1] = static_cast<int>(v[1]);
+            cu_back[b + 1] = static_cast<int>(v[2]);
+        }
+        __syncthreads();
+    }
+    if (tid == 0) cu_q[0] = cu_take[0] = cu_back[0] = 0;
+    __syncthreads();
+
+    const int64_t count = *a.free_count;
+    const int64_t held = count + carry[2];
+    int status = bad;
+    if (!status && (count < 0 || held > a.capacity)) status = 4;
+    if (!status && (carry[0] > a.max_tokens || carry[0] > 0x7FFFFFFF)) status = 3;
+    if (!status && carry[1] > held) status = 1;
+    const bool ok = status == 0;
+    const int tokens = ok ? static_cast<int>(carry[0]) : 0;
+    const int taken = ok ? static_cast<int>(carry[1]) : 0;
+    const int returned = ok ? static_cast<int>(carry[2]) : 0;
+
+    // The page at place i of the stack after the returned pages were pushed.
+    auto stack_at = [&](int64_t i) -> int {
+        if (i < count) return a.free_pages[i];
+        const int r = static_cast<int>(i - count);
+        const int b = find(cu_back, a.B, r);
+        return a.table[b * a.max_pages + (r - cu_back[b])];
+    };
+    auto taken_page = [&](int p) -> int { return stack_at(held - 1 - p); };
+
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
+    for (int64_t t = first; t < a.max_tokens; t += step) {
+        long long slot = -1;
+        int pos = -1;
+        if (t < tokens) {
+            const int b = find(cu_q, a.B, static_cast<int>(t));
+            const int c = a.cached[b];
+            pos = c + static_cast<int>(t) - cu_q[b];
+            const int have = static_cast<int>((c + mask) >> a.page_shift);
+            const int j = pos >> a.page_shift;
+            const int id = j < have ? a.table[b * a.max_pages + j] : taken_page(cu_take[b] + j - have);
+            slot = (static_cast<long long>(id) << a.page_shift) + (pos & mask);
+        }
+        a.slots[t] = slot;
+        a.positions[t] = pos;
+    }
+    for (int64_t p = first; p < taken; p += step) {
+        const int b = find(cu_take, a.B, static_cast<int>(p));
+        const int have = static_cast<int>((a.cached[b] + mask) >> a.page_shift);
+        a.table[b * a.max_pages + have + static_cast<int>(p) - cu_take[b]] = taken_page(static_cast<int>(p));
+    }
+    for (int64_t r = first; r < returned; r += step) {
+        const int b = find(cu_back, a.B, static_cast<int>(r));
+        a.free_pages[count + r] = a.table[b * a.max_pages + (static_cast<int>(r) - cu_back[b])];
+    }
+    for (int64_t b = first; b <= a.B; b += step) {
+        a.cu_q[b] = ok ? cu_q[b] : 0;
+        if (b < a.B) {
+            const int c = a.cached[b], n = a.fresh[b];
+            a.seq_lens[b] = !ok ? c : n < 0 ? 0 : c + n;
+        }
+    }
+    if (first == 0) {
+        a.result[0] = static_cast<int>(ok ? held - taken : count);
+        a.result[1] = taken;
+        a.result[2] = tokens;
+        a.result[3] = status;
+    }
+}
+
+// ------------------------------------------------------------------ append, read
+// 16 channels a thread, D / 16 neighbouring lanes a row; the rows of keys come
+// first, then those of values.  Bound by the bytes: 2 D read and D / 2 + 2
+// written a row (append).
+constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ bool slot_ok(const Cache &c, long long slot) {
+    if (slot < 0) return false;
+    if (slot >= (c.num_pages << c.page_shift)) {
+        page_error();
+        return false;
+    }
+    return true;
+}
+
+// Row index of (slot, head) in the codes and scales.
+__device__ __forceinline__ int64_t row_at(const Cache &c, long long slot, int h) {
+    const int64_t id = slot >> c.page_shift, off = slot & ((1 << c.page_shift) - 1);
+    return ((id * c.heads + h) << c.page_shift) + off;
+}
+
+__global__ void __launch_bounds__(kRowThreads)
+append_kernel(Cache c, const uint16_t *__restrict__ k, int64_t ldk, const uint16_t *__restrict__ v,
+              int64_t ldv, const long long *__restrict__ slots, int64_t T) {
+    const int lanes = c.D / 16;
+    const int64_t half = T * c.heads * lanes, total = 2 * half;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+    const float norm = frag::norm_of(c.group);
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < total; i0 += step) {
+        const int64_t i = i0 + threadIdx.x;
+        const bool values = i >= half;
+        const int64_t row = (values ? i - half : i) / lanes;
+        const int part = static_cast<int>(i % lanes);
+        const int64_t t = row / c.heads;
+        const int h = static_cast<int>(row % c.heads);
+        const long long slot = i < total ? slots[t] : -1;
+        const bool live = slot_ok(c, slot);
+        float x[16] = {};
+        if (live) frag::load16((values ? v + t * ldv : k + t * ldk) + h * c.D + 16 * part, x);
+        frag::rotate16(x, c.group == 256);
+        const uint32_t amax = frag::absmax_bits(x, lanes);
+        float factor;
+        const uint16_t s = frag::block_scale(amax, norm, factor);
+        uint32_t packed[2];
+        prep::quantize_pack(x, factor, packed);
+        if (live) {
+            const int64_t at = row_at(c, slot, h);
+            uint8_t *codes = (values ? c.vc : c.kc) + at * (c.D / 2) + 8 * part;
+            *reinterpret_cast<uint2 *>(codes) = make_uint2(packed[0], packed[1]);
+            if (part == 0) (values ? c.vs : c.ks)[at] = s;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kRowThreads)
+read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *__restrict__ k,
+            uint16_t *__restrict__ v) {
+    const int lanes = c.D / 16;
+    const int64_t half = T * c.heads * lanes, total = 2 * half;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+    const float norm = frag::norm_of(c.group);
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < total; i0 += step) {
+        const int64_t i = i0 + threadIdx.x;
+        const bool values = i >= half;
+        const int64_t row = (values ? i - half : i) / lanes;
+        const int part = static_cast<int>(i % lanes);
+        const long long slot = i < total ? slots[row / c.heads] : -1;
+        float x[16] = {};
+        float s = 0.0f;
+        if (slot_ok(c, slot)) {
+            const int64_t at = row_at(c, slot, static_cast<int>(row % c.heads));
+            const uint2 w = *reinterpret_cast<const uint2 *>((values ? c.vc : c.kc) + at * (c.D / 2) + 8 * part);
+            s = frag::bf16_f32((values ? c.vs : c.ks)[at]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = static_cast<float>(static_cast<int>(w.x << (28 - 4 * e)) >> 28);
+                x[8 + e] = static_cast<float>(static_cast<int>(w.y << (28 - 4 * e)) >> 28);
+            }
+        }
+        // sums of up to 256 codes are exact, and so is their product with
+        // the 8-bit significand of the scale: one rounding, to bf16
+        frag::rotate16(x, c.group == 256);
+        if (i < total) frag::store16((values ? v : k) + row * c.D + 16 * part, x, s * norm);
+    }
+}
+
+// ------------------------------------------------------------------ attention
+// Per request and shared head, the rows are the queries of the heads that
+// share it times the new tokens, in blocks of ROWS = 8 NT; the keys go by in
+// tiles of 64, one tile a warp at a time, with the running maximum and sum of
+// a softmax in fp32:
+//   S^T (64 keys x ROWS) = K (codes, f16) Q^T          mma, A = codes
+//   P = exp2(S s_k - max);  O^T (D x ROWS) += V^T (codes, bf16) (P s_v)^T
+// Codes are the A operand of both products (16 rows an instruction against 8
+// of the B side), so one instruction takes 256 codes.  K's scale goes into the
+// scores and V's into P, both in fp32.
+//
+// The queries are f16, scaled by a power of two that puts the row's largest
+// value at 2^14 .. 2^15 and taken out again in fp32: their rounding is
+// 2^-12 relative, a power below bf16's by eight.  P s_v is rounded to bf16
+// (2^-9 relative, independent from key to key): its range is that of s_v,
+// which f16 could not hold.
+//
+// Which keys of a 16-key block sit in which row of the product is free as
+// long as both products agree.  Row r holds key sigma(r), chosen so that both
+// the 16-byte reads of K and the 4 D/64-byte reads of V spread over the banks.
+//
+// Work.  Units of one tile for one (request, head, row block) are laid out in
+// one line; CTA c takes units [c S, (c + 1) S), so ragged lengths load the
+// GPU evenly and long requests are split.  A CTA whose part ends inside a
+// request writes (max, sum, O) to the workspace and combine_kernel joins the
+// parts in their order.
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kTile = 64;
+constexpr int kMaxCtas = 592;
+constexpr int kMinUnits = kAttnWarps;   // at least one tile a warp
+
+struct AttnArgs {
+    Cache c;
+    const uint16_t *q;
+    int64_t ldq;
+    int64_t T;
+    int G;                   // query heads that share a head
+    const int *table;
+    int64_t max_pages;
+    const int *seq_lens, *cu_q;
+    int B;
+    float scale;             // softmax scale * log2(e)
+    int4 *desc;              // per CTA: {last CTA of the request it starts and does not end, b, h, row block}
+    float *parts;            // per CTA two parts: ROWS (max, sum), then ROWS x D
+    uint16_t *out;
+};
+
+__device__ __forceinline__ int sigma(int g) { return (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1; }
+
+struct Request {
+    int len, q0, nq, tiles, blocks;
+};
+
+// Request b's sizes, clamped to what its buffers hold.
+template <int ROWS>
+__device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
+    Request r;
+    int64_t len = a.seq_lens[b];
+    const int64_t most = a.max_pages << a.c.page_shift;
+    len = len < 0 ? 0 : len > most ? most : len;
+    int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+    q0 = q0 < 0 ? 0 : q0;
+    q1 = q1 > a.T ? a.T : q1;
+    r.len = static_cast<int>(len);
+    r.q0 = static_cast<int>(q0);
+    r.nq = q1 > q0 ? static_cast<int>(q1 - q0) : 0;
+    r.tiles = len > 0 ? (r.len - 1) / kTile + 1 : 1;
+    r.blocks = static_cast<int>((static_cast<int64_t>(r.nq) * a.G + ROWS - 1) / ROWS);
+    return r;
+}
+
+// Output row r of a row block -> rotate back 16 channels a thread and store.
+__device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, int h, int row,
+                                          int part, float (&x)[16], float total) {
+    frag::rotate16(x, a.c.group == 256);
+    const int i = row / a.G;
+    if (i < rq.nq) {
+        const float f = total > 0.0f || total != total ? frag::norm_of(a.c.group) / total : 0.0f;
+        const int heads = a.G * a.c.heads;
+        frag::store16(a.out + ((static_cast<int64_t>(rq.q0) + i) * heads + h * a.G + row % a.G) * a.c.D + 16 * part, x, f);
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
+    constexpr int ROWS = 8 * NT;
+    constexpr int NW = D / 32;          // K words (8 codes) a thread and key
+    constexpr int VW = D / 64;          // V words a thread and key
+    constexpr int MT = D / 16;          // 16-row blocks of O^T
+    constexpr int LANES = D / 16;
+    constexpr int PITCH = D + 4;
+    extern __shared__ uint4 smem[];
+    // queries as B fragments: [NT][NW][32 lanes] of 16 bytes
+    uint4 *qf = smem;
+    float *osum = reinterpret_cast<float *>(smem + NT * NW * 32);   // [warps][ROWS][PITCH]
+    __shared__ float qs[ROWS];
+    __shared__ int qmax[ROWS];
+    __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS];
+    __shared__ long long scan[kAttnWarps];
+    __shared__ long long start_unit;
+    __shared__ int start_b;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+
+    // ---- this CTA's part of the line of units
+    const int chunk = (a.B + kAttnThreads - 1) / kAttnThreads;
+    const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const Request r = request_of<ROWS>(a, b);
+        mine += static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
+    }
+    long long incl = mine;
+    for (int s = 1; s < 32; s <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, s);
+        if (lane >= s) incl += u;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < kMinUnits) share = kMinUnits;
+    const long long u0 = share * blockIdx.x;
+    const long long u1 = min(u0 + share, total);
+    if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (u0 >= total) return;
+    if (mine > 0 && before <= u0 && u0 < before + mine) {
+        long long at = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const Request r = request_of<ROWS>(a, b);
+            const long long n = static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
+            if (u0 < at + n) {
+                start_b = b;
+                start_unit = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    int b = start_b;
+    long long base = start_unit;        // first unit of request b
+
+    for (long long u = u0; u < u1;) {
+        Request rq = request_of<ROWS>(a, b);
+        long long n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
+        while (u >= base + n) {
+            base += n;
+            if (++b >= a.B) return;     // lengths that changed under the kernel
+            rq = request_of<ROWS>(a, b);
+            n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
+        }
+        const int seg = static_cast<int>((u - base) / rq.tiles);
+        const int tile0 = static_cast<int>((u - base) % rq.tiles);
+        const long long seg_u0 = base + static_cast<long long>(seg) * rq.tiles, seg_u1 = seg_u0 + rq.tiles;
+        const int tile1 = static_cast<int>(min(u1, seg_u1) - seg_u0);
+        const int h = seg / rq.blocks, rb = seg % rq.blocks;
+        const int row0 = rb * ROWS;
+
+        __syncthreads();                // the last request's shared data is done with
+        // ---- queries: rotate, scale to f16, lay out as B fragments
+        for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
+            const int i = i0 + tid;
+            const int r = i / LANES, part = i % LANES;
+            const int qi = (row0 + r) / a.G, hd = h * a.G + (row0 + r) % a.G;
+            const bool live = r < ROWS && qi < rq.nq;
+            float x[16] = {};
+            if (live) frag::load16(a.q + (static_cast<int64_t>(rq.q0) + qi) * a.ldq + static_cast<int64_t>(hd) * D + 16 * part, x);
+            frag::rotate16(x, a.c.group == 256);
+            const uint32_t amax = frag::absmax_bits(x, LANES);
+            // 2^(14 - floor(log2 amax)), its exponent kept in range
+            const int e = min(254, 127 + 14 - (static_cast<int>(amax >> 23) - 127));
+            const float f = amax ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
+            if (r < ROWS) {
+                if (part == 0) {
+                    qs[r] = amax ? a.scale * frag::norm_of(a.c.group) * __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 0.0f;
+                    qmax[r] = rq.len - rq.nq + min(qi, rq.nq - 1);   // rows past the last query are not stored
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int d = 16 * part + 8 * half;
+                    const int tq = D == 64 ? d / 16 : (d % 128) / 32;
+                    const int j = D == 64 ? (d % 16) / 8 : 4 * (d / 128) + (d % 32) / 8;
+                    const float *y = x + 8 * half;
+                    qf[((r >> 3) * NW + j) * 32 + (r & 7) * 4 + tq] =
+                        make_uint4(frag::pack_f16(y[0] * f, y[4] * f), frag::pack_f16(y[1] * f, y[5] * f),
+                                   frag::pack_f16(y[2] * f, y[6] * f), frag::pack_f16(y[3] * f, y[7] * f));
+                }
+            }
+        }
+        __syncthreads();
+
+        // thread's columns: queries 8 nt + 2 t4 and + 1
+        float cs[NT][2];
+        int cmax[NT][2];
+        int least = 0x7FFFFFFF;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                cs[nt][x] = qs[8 * nt + 2 * t4 + x];
+                cmax[nt][x] = qmax[8 * nt + 2 * t4 + x];
+                least = min(least, cmax[nt][x]);
+            }
+        for (int s = 1; s < 4; s <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, s));
+
+        float o[MT][NT][4] = {};
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                m[nt][x] = -INFINITY;
+                l[nt][x] = 0.0f;
+            }
+        const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
+
+        for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
+            const int k0 = tile * kTile;
+            float s[4][NT][4] = {};
+            int64_t rows[4];            // first cache row of each 16-key block, -1: none
+            float sv[4][2];
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+                const int j0 = k0 + 16 * blk;
+                rows[blk] = -1;
+                sv[blk][0] = sv[blk][1] = 0.0f;
+                if (j0 < rq.len) {
+                    const int id = table[j0 >> a.c.page_shift];
+                    if (id >= 0 && id < a.c.num_pages)
+                        rows[blk] = ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) +
+                                    (j0 & ((1 << a.c.page_shift) - 1));
+                    else if (lane == 0) page_error();
+                }
+                uint32_t ka[NW] = {}, kb[NW] = {};
+                float sk[2] = {0.0f, 0.0f};
+                if (rows[blk] >= 0) {
+                    const int64_t ra = rows[blk] + sigma(g), rbw = ra + 8;
+                    sk[0] = frag::bf16_f32(a.c.ks[ra]);
+                    sk[1] = frag::bf16_f32(a.c.ks[rbw]);
+                    sv[blk][0] = frag::bf16_f32(a.c.vs[ra]);
+                    sv[blk][1] = frag::bf16_f32(a.c.vs[rbw]);
+                    const uint8_t *pa = a.c.kc + ra * (D / 2), *pb = a.c.kc + rbw * (D / 2);
+                    if constexpr (D == 64) {
+                        *reinterpret_cast<uint2 *>(ka) = *reinterpret_cast<const uint2 *>(pa + 8 * t4);
+                        *reinterpret_cast<uint2 *>(kb) = *reinterpret_cast<const uint2 *>(pb + 8 * t4);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NW / 4; ++i) {
+                            reinterpret_cast<uint4 *>(ka)[i] = *reinterpret_cast<const uint4 *>(pa + 64 * i + 16 * t4);
+                            reinterpret_cast<uint4 *>(kb)[i] = *reinterpret_cast<const uint4 *>(pb + 64 * i + 16 * t4);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NW; ++j) {
+                    uint32_t wa[4], wb[4];
+                    frag::widen_f16(ka[j], wa);
+                    frag::widen_f16(kb[j], wb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint4 q = qf[(nt * NW + j) * 32 + lane];
+                        frag::mma_f16(s[blk][nt], wa[0], wb[0], wa[1], wb[1], q.x, q.y);
+                        frag::mma_f16(s[blk][nt], wa[2], wb[2], wa[3], wb[3], q.z, q.w);
+                    }
+                }
+                // scores in units of log2; hidden keys are -inf whatever they hold
+                const int ja = j0 + sigma(g), jb = ja + 8;
+                const bool all = rows[blk] >= 0 && j0 + 15 <= least;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        s[blk][nt][x] *= sk[0] * cs[nt][x];
+                        s[blk][nt][2 + x] *= sk[1] * cs[nt][x];
+                        if (!all) {
+                            if (rows[blk] < 0 || ja > cmax[nt][x]) s[blk][nt][x] = -INFINITY;
+                            if (rows[blk] < 0 || jb > cmax[nt][x]) s[blk][nt][2 + x] = -INFINITY;
+                        }
+                    }
+            }
+            // ---- running maximum and sum
+            float mul[NT][2];
+            bool turn = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float top = m[nt][x];
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk) top = fmaxf(top, fmaxf(s[blk][nt][x], s[blk][nt][2 + x]));
+                    for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+                    const float safe = top == -INFINITY ? 0.0f : top;
+                    mul[nt][x] = exp2f(m[nt][x] - safe);
+                    turn |= top != m[nt][x];
+                    m[nt][x] = top;
+                    l[nt][x] *= mul[nt][x];
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk)
+#pragma unroll
+                        for (int y = 0; y < 4; y += 2) {
+                            const float p = exp2f(s[blk][nt][y + x] - safe);
+                            l[nt][x] += p;
+                            // a hidden key's scale may be anything
+                            s[blk][nt][y + x] = s[blk][nt][y + x] == -INFINITY ? 0.0f : p * sv[blk][y >> 1];
+                        }
+                }
+            if (__any_sync(0xFFFFFFFFu, turn)) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= mul[nt][x & 1];
+            }
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+                if (rows[blk] < 0) continue;
+                uint32_t p0[NT], p1[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    p0[nt] = frag::transpose8x8(frag::pack_bf16(s[blk][nt][0], s[blk][nt][1]));
+                    p1[nt] = frag::transpose8x8(frag::pack_bf16(s[blk][nt][2], s[blk][nt][3]));
+                }
+                // columns 2 t4, 2 t4 + 1 of the product are the keys sigma of those
+                uint32_t v[4][VW];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = sigma(2 * t4 + (i & 1)) + 8 * (i >> 1);
+                    const uint8_t *p = a.c.vc + (rows[blk] + key) * (D / 2) + 4 * VW * g;
+                    if constexpr (VW == 1) v[i][0] = *reinterpret_cast<const uint32_t *>(p);
+                    else if constexpr (VW == 2) *reinterpret_cast<uint2 *>(v[i]) = *reinterpret_cast<const uint2 *>(p);
+                    else *reinterpret_cast<uint4 *>(v[i]) = *reinterpret_cast<const uint4 *>(p);
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    // halves of two keys side by side: codes 0-3, then 4-7
+                    uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
+                    frag::widen_bf16(__byte_perm(v[0][w], v[1][w], 0x5410), lo0);
+                    frag::widen_bf16(__byte_perm(v[0][w], v[1][w], 0x7632), hi0);
+                    frag::widen_bf16(__byte_perm(v[2][w], v[3][w], 0x5410), lo1);
+                    frag::widen_bf16(__byte_perm(v[2][w], v[3][w], 0x7632), hi1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            frag::mma_bf16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p0[nt], p1[nt]);
+                }
+            }
+        }
+
+        // ---- join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                for (int k = 4; k < 32; k <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], k);
+                if (g == 0) {
+                    wm[warp][8 * nt + 2 * t4 + x] = m[nt][x];
+                    wl[warp][8 * nt + 2 * t4 + x] = l[nt][x];
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    osum[(warp * ROWS + 8 * nt + 2 * t4 + (x & 1)) * PITCH + (D / 8) * g + 8 * (i >> 2) + (i & 3) +
+                         4 * (x >> 1)] = o[i][nt][x];
+        __syncthreads();
+        const bool whole = seg_u0 >= u0 && seg_u1 <= u1;
+        float *part_out = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (seg_u0 >= u0 ? 1 : 0)) * (ROWS * (D + 2));
+        for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
+            const int i = i0 + tid;
+            const int r = min(i / LANES, ROWS - 1), part = i % LANES;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, wm[w][r]);
+            const float safe = top == -INFINITY ? 0.0f : top;
+            float x[16] = {}, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = exp2f(wm[w][r] - safe);
+                sum += f * wl[w][r];
+                const float4 *src = reinterpret_cast<const float4 *>(osum + (w * ROWS + r) * PITCH + 16 * part);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 y = src[e];
+                    x[4 * e] += f * y.x;
+                    x[4 * e + 1] += f * y.y;
+                    x[4 * e + 2] += f * y.z;
+                    x[4 * e + 3] += f * y.w;
+                }
+            }
+            if (whole) {
+                store_row(a, rq, h, i < ROWS * LANES ? row0 + r : 0x7FFFFFFF, part, x, sum);
+            } else if (i < ROWS * LANES) {
+                if (part == 0) {
+                    part_out[2 * r] = top;
+                    part_out[2 * r + 1] = sum;
+                }
+                float4 *dst = reinterpret_cast<float4 *>(part_out + 2 * ROWS + r * D + 16 * part);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+        }
+        if (!whole && seg_u0 >= u0 && tid == 0)
+            a.desc[blockIdx.x] = make_int4(static_cast<int>((seg_u1 - 1) / share), b, h, rb);
+        u = seg_u0 + tile1;
+    }
+}
+
+// CTA c joins the parts of the request that CTA c of attention_kernel began
+// and did not end.
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
+    constexpr int ROWS = 8 * NT, LANES = D / 16;
+    ptx::grid_dependency_wait();
+    const int4 d = a.desc[blockIdx.x];
+    if (d.x < 0) return;
+    const Request rq = request_of<ROWS>(a, d.y);
+    for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        const int r = min(i / LANES, ROWS - 1), part = i % LANES;
+        float x[16] = {}, sum = 0.0f, top = -INFINITY;
+        for (int c = blockIdx.x; c <= d.x; ++c) {
+            const float *p = a.parts + (2 * static_cast<int64_t>(c) + (c == static_cast<int>(blockIdx.x) ? 1 : 0)) * (ROWS * (D + 2));
+            const float mc = p[2 * r], lc = p[2 * r + 1];
+            const float next = fmaxf(top, mc);
+            const float safe = next == -INFINITY ? 0.0f : next;
+            const float fo = exp2f(top - safe), fn = exp2f(mc - safe);
+            top = next;
+            sum = sum * fo + lc * fn;
+            const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 y = src[e];
+                x[4 * e] = x[4 * e] * fo + y.x * fn;
+                x[4 * e + 1] = x[4 * e + 1] * fo + y.y * fn;
+                x[4 * e + 2] = x[4 * e + 2] * fo + y.z * fn;
+                x[4 * e + 3] = x[4 * e + 3] * fo + y.w * fn;
+            }
+        }
+        store_row(a, rq, d.z, i < ROWS * LANES ? d.w * ROWS + r : 0x7FFFFFFF, part, x, sum);
+    }
+}
+
+template <int D, int NT>
+constexpr int attn_smem() {
+    return NT * (D / 32) * 512 + kAttnWarps * 8 * NT * (D + 4) * 4;
+}
+
+}  // namespace kv4
+
+// ====================================================================== host
+
+namespace {
+
+using namespace kv4;
+
+template <class F>
+bool set_smem(F *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+convrot_status setup(int *dev) {
+    return host::device_setup(dev, [] {
+        bool ok = set_smem(plan_kernel, 3 * (CONVROT_KV4_MAX_REQUESTS + 1) * 4);
+        ok &= set_smem(attention_kernel<64, 1>, attn_smem<64, 1>());
+        ok &= set_smem(attention_kernel<64, 2>, attn_smem<64, 2>());
+        ok &= set_smem(attention_kernel<64, 4>, attn_smem<64, 4>());
+        ok &= set_smem(attention_kernel<128, 1>, attn_smem<128, 1>());
+        ok &= set_smem(attention_kernel<128, 2>, attn_smem<128, 2>());
+        ok &= set_smem(attention_kernel<128, 4>, attn_smem<128, 4>());
+        ok &= set_smem(attention_kernel<256, 1>, attn_smem<256, 1>());
+        ok &= set_smem(attention_kernel<256, 2>, attn_smem<256, 2>());
+        return ok;
+    });
+}
+
+int shift_of(int page) {
+    for (int s = 4; s <= 8; ++s)
+        if (page == 1 << s) return s;
+    return -1;
+}
+
+convrot_status check_cache(const convrot_kv4_cache *c) {
+    if (!c) return CONVROT_ERR_NULL;
+    if (c->group != 64 && c->group != 256) return CONVROT_ERR_GROUP;
+    if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->head_dim % c->group)
+        return CONVROT_ERR_SHAPE;
+    if (shift_of(c->page) < 0 || c->kv_heads < 1 || c->kv_heads > 1024 || c->num_pages < 0 ||
+        c->num_pages >= (int64_t(1) << 31) / c->page)
+        return CONVROT_ERR_SHAPE;
+    return CONVROT_OK;
+}
+
+// Pointers of a cache with at least one page.
+convrot_status check_cache_ptrs(const convrot_kv4_cache *c) {
+    if (!c->num_pages) return CONVROT_OK;
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return CONVROT_ERR_NULL;
+    return host::aligned16({c->k_codes, c->k_scales, c->v_codes, c->v_scales}) ? CONVROT_OK : CONVROT_ERR_ALIGN;
+}
+
+Cache device_cache(const convrot_kv4_cache *c) {
+    return Cache{c->k_codes, static_cast<uint16_t *>(c->k_scales), c->v_codes,
+                 static_cast<uint16_t *>(c->v_scales), c->num_pages, c->kv_heads,
+                 shift_of(c->page), c->head_dim, c->group};
+}
+
+convrot_status launched() {
+    return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
+}
+
+// Grid of a grid-stride kernel: one pass, up to eight CTAs an SM.
+unsigned row_grid(int64_t threads, int sms) {
+    const int64_t n = (threads + kRowThreads - 1) / kRowThreads;
+    return static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
+}
+
+// Query columns of the product: the smallest of 8, 16 and 32 (16 with D = 256,
+// whose accumulators fill the registers) that holds an average request's rows.
+int row_tiles(int64_t T, int64_t B, int G, int D) {
+    const int64_t rows = (T + B - 1) / B * G;
+    return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
+}
+
+// CTAs that can have work at most, from what the host knows.
+int64_t attn_ctas(int64_t T, int64_t B, int G, int kv_heads, int NT, int64_t max_keys) {
+    const int64_t blocks = (T * G + 8 * NT - 1) / (8 * NT) + B;
+    const int64_t tiles = (max_keys + kTile - 1) / kTile;
+    // beyond kMaxCtas the product is not needed, and could overflow
+    if (blocks > 8 * kMaxCtas || tiles > 8 * kMaxCtas) return kMaxCtas;
+    const int64_t n = (blocks * (tiles > 0 ? tiles : 1) * kv_heads + kMinUnits - 1) / kMinUnits;
+    return n < kMaxCtas ? n : kMaxCtas;
+}
+
+bool attn_shape_ok(int64_t T, int64_t B, int heads, int kv_heads, int D, int64_t max_keys) {
+    return T >= 0 && B >= 0 && B <= CONVROT_KV4_MAX_REQUESTS && T < (int64_t(1) << 31) && kv_heads >= 1 &&
+           kv_heads <= 1024 && heads >= kv_heads && heads % kv_heads == 0 && heads <= 65536 &&
+           (D == 64 || D == 128 || D == 256) && max_keys >= 0 && max_keys < (int64_t(1) << 31);
+}
+
+template <int D, int NT>
+convrot_status launch_attention(AttnArgs a, int64_t ctas, int sms, cudaStream_t stream) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_kernel<D, NT>, kAttnThreads,
+                                                      attn_smem<D, NT>()) != cudaSuccess)
+        return CONVROT_ERR_CUDA;
+    if (ctas > static_cast<int64_t>(sms) * per_sm) ctas = static_cast<int64_t>(sms) * per_sm;
+    attention_kernel<D, NT><<<static_cast<unsigned>(ctas), kAttnThreads, attn_smem<D, NT>(), stream>>>(a);
+    if (launched() != CONVROT_OK) return CONVROT_ERR_CUDA;
+    return host::launch_dependent(combine_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), dim3(kAttnThreads), 0,
+                                  stream, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+convrot_status convrot_kv4_plan(const int32_t *cached, const int32_t *new_tokens, int64_t B,
+                                int page, int32_t *block_table, int64_t max_pages,
+                                int32_t *free_pages, int64_t capacity, const int32_t *free_count,
+                                int64_t max_tokens, int32_t *seq_lens, int32_t *cu_q,
+                                int64_t *slots, int32_t *positions, int32_t *result,
+                                convrot_stream_t stream) {
+    const int shift = shift_of(page);
+    if (B < 1 || B > CONVROT_KV4_MAX_REQUESTS || shift < 0 || max_pages < 0 || max_pages >= (int64_t(1) << 31) ||
+        capacity < 0 || capacity >= (int64_t(1) << 31) || max_tokens < 0 || max_tokens >= (int64_t(1) << 31))
+        return CONVROT_ERR_SHAPE;
+    if (!cached || !new_tokens || !free_count || !seq_lens || !cu_q || !result || (max_pages && !block_table) ||
+        (capacity && !free_pages) || (max_tokens && (!slots || !positions)))
+        return CONVROT_ERR_NULL;
+    if (!host::aligned16({cached, new_tokens, block_table, free_pages, free_count, seq_lens, cu_q, slots, positions, result}))
+        return CONVROT_ERR_ALIGN;
+    int dev;
+    convrot_status st = setup(&dev);
+    if (st != CONVROT_OK) return st;
+    if ((st = host::check_device_ptrs(dev, {cached, new_tokens, block_table, free_pages, free_count, seq_lens, cu_q,
+                                            slots, positions, result})) != CONVROT_OK)
+        return st;
+    PlanArgs a{cached, new_tokens, static_cast<int>(B), shift, block_table, max_pages, free_pages, capacity,
+               free_count, max_tokens, seq_lens, cu_q, reinterpret_cast<long long *>(slots), positions, result};
+    int64_t grid = (max_tokens + kPlanThreads - 1) / kPlanThreads;
+    const int sms = host::g_dev[dev].num_sms;
+    grid = grid < 1 ? 1 : grid > sms ? sms : grid;
+    plan_kernel<<<static_cast<unsigned>(grid), kPlanThreads, 3 * (B + 1) * 4, stream>>>(a);
+    return launched();
+}
+
+convrot_status convrot_kv4_append(const convrot_kv4_cache *cache, const void *k_bf16, int64_t ldk,
+                                  const void *v_bf16, int64_t ldv, const int64_t *slots, int64_t T,
+                                  convrot_stream_t stream) {
+    convrot_status st = check_cache(cache);
+    if (st != CONVROT_OK) return st;
+    const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+    if (T < 0 || T >= (int64_t(1) << 31) || ldk < width || ldv < width || ldk % 8 || ldv % 8) return CONVROT_ERR_SHAPE;
+    if (T == 0) return CONVROT_OK;
+    if (!k_bf16 || !v_bf16 || !slots) return CONVROT_ERR_NULL;
+    if ((st = check_cache_ptrs(cache)) != CONVROT_OK) return st;
+    if (!host::aligned16({k_bf16, v_bf16, slots})) return CONVROT_ERR_ALIGN;
+    int dev;
+    if ((st = setup(&dev)) != CONVROT_OK) return st;
+    if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
+                                            cache->v_scales})) != CONVROT_OK)
+        return st;
+    append_kernel<<<row_grid(2 * T * width / 16, host::g_dev[dev].num_sms), kRowThreads, 0, stream>>>(
+        device_cache(cache), static_cast<const uint16_t *>(k_bf16), ldk, static_cast<const uint16_t *>(v_bf16), ldv,
+        reinterpret_cast<const long long *>(slots), T);
+    return launched();
+}
+
+convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *slots, int64_t T,
+                                void *k_bf16, void *v_bf16, convrot_stream_t stream) {
+    convrot_status st = check_cache(cache);
+    if (st != CONVROT_OK) return st;
+    if (T < 0 || T >= (int64_t(1) << 31)) return CONVROT_ERR_SHAPE;
+    if (T == 0) return CONVROT_OK;
+    if (!k_bf16 || !v_bf16 || !slots) return CONVROT_ERR_NULL;
+    if ((st = check_cache_ptrs(cache)) != CONVROT_OK) return st;
+    if (!host::aligned16({k_bf16, v_bf16, slots})) return CONVROT_ERR_ALIGN;
+    int dev;
+    if ((st = setup(&dev)) != CONVROT_OK) return st;
+    if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
+                                            cache->v_scales})) != CONVROT_OK)
+        return st;
+    const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+    read_kernel<<<row_grid(2 * T * width / 16, host::g_dev[dev].num_sms), kRowThreads, 0, stream>>>(
+        device_cache(cache), reinterpret_cast<const long long *>(slots), T, static_cast<uint16_t *>(k_bf16),
+        static_cast<uint16_t *>(v_bf16));
+    return launched();
+}
+
+size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int kv_heads,
+                                            int head_dim, int64_t max_keys) {
+    if (!attn_shape_ok(T, B, heads, kv_heads, head_dim, max_keys) || T == 0 || B == 0) return 0;
+    const int G = heads / kv_heads, NT = row_tiles(T, B, G, head_dim);
+    const size_t ctas = static_cast<size_t>(attn_ctas(T, B, G, kv_heads, NT, max_keys));
+    return host::round256(ctas * sizeof(int4)) + ctas * 2 * 8 * NT * (head_dim + 2) * sizeof(float);
+}
+
+convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void *q_bf16,
+                                     int64_t ldq, int64_t T, int heads, const int32_t *block_table,
+                                     int64_t max_pages, const int32_t *seq_lens,
+                                     const int32_t *cu_q, int64_t B, float scale, void *workspace,
+                                     size_t ws_bytes, void *out_bf16, convrot_stream_t stream) {
+    convrot_status st = check_cache(cache);
+    if (st != CONVROT_OK) return st;
+    const int D = cache->head_dim;
+    if (max_pages < 0 || max_pages >= (int64_t(1) << 31) / cache->page ||
+        !attn_shape_ok(T, B, heads, cache->kv_heads, D, max_pages * cache->page) ||
+        ldq < static_cast<int64_t>(heads) * D || ldq % 8 || !(scale - scale == 0.0f))
+        return CONVROT_ERR_SHAPE;
+    if (T == 0 || B == 0) return CONVROT_OK;
+    if (!q_bf16 || !seq_lens || !cu_q || !out_bf16 || !workspace || (max_pages && !block_table)) return CONVROT_ERR_NULL;
+    if ((st = check_cache_ptrs(cache)) != CONVROT_OK) return st;
+    if (ws_bytes < convrot_kv4_attention_workspace_size(T, B, heads, cache->kv_heads, D, max_pages * cache->page) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return CONVROT_ERR_WORKSPACE;
+    if (!host::aligned16({q_bf16, block_table, seq_lens, cu_q, out_bf16})) return CONVROT_ERR_ALIGN;
+    int dev;
+    if ((st = setup(&dev)) != CONVROT_OK) return st;
+    if ((st = host::check_device_ptrs(dev, {q_bf16, block_table, seq_lens, cu_q, out_bf16, workspace, cache->k_codes,
+                                            cache->k_scales, cache->v_codes, cache->v_scales})) != CONVROT_OK)
+        return st;
+    const int G = heads / cache->kv_heads, NT = row_tiles(T, B, G, D);
+    const int64_t ctas = attn_ctas(T, B, G, cache->kv_heads, NT, max_pages * cache->page);
+    AttnArgs a{device_cache(cache), static_cast<const uint16_t *>(q_bf16), ldq, T, G, block_table, max_pages,
+               seq_lens, cu_q, static_cast<int>(B), scale * 1.4426950408889634f, static_cast<int4 *>(workspace),
+               reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(ctas * sizeof(int4))),
+               static_cast<uint16_t *>(out_bf16)};
+    const int sms = host::g_dev[dev].num_sms;
+    if (D == 64)
+        return NT == 1 ? launch_attention<64, 1>(a, ctas, sms, stream)
+                       : NT == 2 ? launch_attention<64, 2>(a, ctas, sms, stream) : launch_attention<64, 4>(a, ctas, sms, stream);
+    if (D == 128)
+        return NT == 1 ? launch_attention<128, 1>(a, ctas, sms, stream)
+                       : NT == 2 ? launch_attention<128, 2>(a, ctas, sms, stream) : launch_attention<128, 4>(a, ctas, sms, stream);
+    return NT == 1 ? launch_attention<256, 1>(a, ctas, sms, stream) : launch_attention<256, 2>(a, ctas, sms, stream);
+}
+
+convrot_status convrot_kv4_check_device_error(convrot_stream_t stream) {
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return CONVROT_ERR_CUDA;
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_convrot_error, sizeof v) != cudaSuccess) return CONVROT_ERR_CUDA;
+    if (v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_convrot_error, &zero, sizeof zero) != cudaSuccess) return CONVROT_ERR_CUDA;
+        return static_cast<convrot_status>(v);
+    }
+    return CONVROT_OK;
+}
+
+}  // extern "C"
