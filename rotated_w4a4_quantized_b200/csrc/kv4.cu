@@ -283,6 +283,11 @@ read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *_
 // long as both products agree.  Row r holds key sigma(r), chosen so that both
 // the 16-byte reads of K and the 4 D/64-byte reads of V spread over the banks.
 //
+// Copies.  Each warp has its own ring of stages (a tile's codes and scales,
+// about 8 KB) filled by bulk copies, one per run of keys in a page and array,
+// that complete on the warp's own barrier: no warp waits for another inside a
+// request, and an SM keeps 200 KB on the way.
+//
 // Work.  Units of one tile for one (request, head, row block) are laid out in
 // one line; CTA c takes units [c S, (c + 1) S), so ragged lengths load the
 // GPU evenly and long requests are split.  A CTA whose part ends inside a
@@ -290,8 +295,13 @@ read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *_
 // parts in their order.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kTile = 64;
 constexpr int kMaxCtas = 592;
+
+// Keys of a tile, and tiles a warp's ring holds: about 8 KB a stage, and the
+// rings of a CTA (three fit an SM) large enough to hold the warps' outputs
+// when they are joined.
+__host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
+__host__ __device__ constexpr int ring_depth(int D) { return D == 64 ? 3 : 2; }
 constexpr int kMinUnits = kAttnWarps;   // at least one tile a warp
 
 struct AttnArgs {
@@ -317,7 +327,7 @@ struct Request {
 };
 
 // Request b's sizes, clamped to what its buffers hold.
-template <int ROWS>
+template <int D, int ROWS>
 __device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
     Request r;
     int64_t len = a.seq_lens[b];
@@ -329,9 +339,23 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
     r.len = static_cast<int>(len);
     r.q0 = static_cast<int>(q0);
     r.nq = q1 > q0 ? static_cast<int>(q1 - q0) : 0;
-    r.tiles = len > 0 ? (r.len - 1) / kTile + 1 : 1;
+    r.tiles = len > 0 ? (r.len - 1) / tile_keys(D) + 1 : 1;
     r.blocks = static_cast<int>((static_cast<int64_t>(r.nq) * a.G + ROWS - 1) / ROWS);
     return r;
+}
+
+// 2^x for x <= 0 (one instruction; results below the normal range are 0).
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Contiguous bytes (16-byte aligned, a multiple of 16) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // Output row r of a row block -> rotate back 16 channels a thread and store.
@@ -354,10 +378,16 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     constexpr int MT = D / 16;          // 16-row blocks of O^T
     constexpr int LANES = D / 16;
     constexpr int PITCH = D + 4;
+    constexpr int TILE = tile_keys(D), NB = TILE / 16, DEPTH = ring_depth(D);
+    constexpr int STAGE = TILE * (D + 4);   // codes of keys, of values, scales of keys, of values
     extern __shared__ uint4 smem[];
     // queries as B fragments: [NT][NW][32 lanes] of 16 bytes
     uint4 *qf = smem;
-    float *osum = reinterpret_cast<float *>(smem + NT * NW * 32);   // [warps][ROWS][PITCH]
+    uint8_t *rings = reinterpret_cast<uint8_t *>(smem + NT * NW * 32);
+    float *osum = reinterpret_cast<float *>(rings);   // [warps][ROWS][PITCH], when the rings are drained
+    static_assert(kAttnWarps * ROWS * PITCH * 4 <= kAttnWarps * DEPTH * STAGE, "outputs fit the rings");
+    __shared__ uint64_t bars[kAttnWarps][DEPTH];
+    __shared__ int abort_flag;
     __shared__ float qs[ROWS];
     __shared__ int qmax[ROWS];
     __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS];
@@ -367,13 +397,17 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
+    if (tid == 0) abort_flag = 0;
+    if (lane == 0)
+        for (int i = 0; i < DEPTH; ++i) ptx::mbar_init(ptx::smem_u32(&bars[warp][i]), 1);
+    ptx::fence_mbar_init();
 
     // ---- this CTA's part of the line of units
     const int chunk = (a.B + kAttnThreads - 1) / kAttnThreads;
     const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-        const Request r = request_of<ROWS>(a, b);
+        const Request r = request_of<D, ROWS>(a, b);
         mine += static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
     }
     long long incl = mine;
@@ -398,7 +432,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     if (mine > 0 && before <= u0 && u0 < before + mine) {
         long long at = before;
         for (int b = b_lo; b < b_hi; ++b) {
-            const Request r = request_of<ROWS>(a, b);
+            const Request r = request_of<D, ROWS>(a, b);
             const long long n = static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
             if (u0 < at + n) {
                 start_b = b;
@@ -411,14 +445,19 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     __syncthreads();
     int b = start_b;
     long long base = start_unit;        // first unit of request b
+    int slot = 0;
+    uint32_t parity = 0;                // of the slot's next completion
+    const uint8_t *ring = rings + warp * (DEPTH * STAGE);
+    const uint32_t ring_s = ptx::smem_u32(ring);
+    const int piece_shift = min(a.c.page_shift, TILE == 64 ? 6 : 5);   // keys of a tile in one page
 
     for (long long u = u0; u < u1;) {
-        Request rq = request_of<ROWS>(a, b);
+        Request rq = request_of<D, ROWS>(a, b);
         long long n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
         while (u >= base + n) {
             base += n;
             if (++b >= a.B) return;     // lengths that changed under the kernel
-            rq = request_of<ROWS>(a, b);
+            rq = request_of<D, ROWS>(a, b);
             n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
         }
         const int seg = static_cast<int>((u - base) / rq.tiles);
@@ -429,6 +468,42 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
         const int row0 = rb * ROWS;
 
         __syncthreads();                // the last request's shared data is done with
+        const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
+        // Request a tile into a slot: lane 4 p + i copies array i of the p-th
+        // run of keys that lie in one page.  Returns a bit for each 16 keys
+        // that are there.
+        auto request = [&](int tile, int at) -> uint32_t {
+            const int p = lane >> 2, which = lane & 3, keys = 1 << piece_shift;
+            const int j0 = tile * TILE + (p << piece_shift);
+            const bool want = tile < tile1 && (p << piece_shift) < TILE && j0 < rq.len;
+            const int id = want ? table[j0 >> a.c.page_shift] : -1;
+            const bool there = want && id >= 0 && id < a.c.num_pages;
+            if (want && !there) page_error();
+            const uint32_t runs = __ballot_sync(0xFFFFFFFFu, there);
+            const uint32_t bar = ptx::smem_u32(&bars[warp][at]);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, __popc(runs & 0x11111111u) * keys * (D + 4));
+            if (there) {
+                const int64_t row = ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) +
+                                    (j0 & ((1 << a.c.page_shift) - 1));
+                const uint32_t dst = ring_s + at * STAGE;
+                if (which < 2)
+                    bulk_load(dst + which * (TILE * D / 2) + (p << piece_shift) * (D / 2),
+                              (which ? a.c.vc : a.c.kc) + row * (D / 2), keys * (D / 2), bar);
+                else
+                    bulk_load(dst + TILE * D + (which - 2) * (TILE * 2) + (p << piece_shift) * 2,
+                              (which == 3 ? a.c.vs : a.c.ks) + row, keys * 2, bar);
+            }
+            uint32_t live = 0;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) live |= ((runs >> (4 * ((16 * i) >> piece_shift))) & 1u) << i;
+            return live;
+        };
+        uint32_t live[DEPTH];
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            const int at = slot + i < DEPTH ? slot + i : slot + i - DEPTH;
+            live[i] = tile0 + warp + i * kAttnWarps < tile1 ? request(tile0 + warp + i * kAttnWarps, at) : 0;
+        }
         // ---- queries: rotate, scale to f16, lay out as B fragments
         for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
             const int i = i0 + tid;
@@ -484,43 +559,26 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 m[nt][x] = -INFINITY;
                 l[nt][x] = 0.0f;
             }
-        const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
-
         for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
-            const int k0 = tile * kTile;
-            float s[4][NT][4] = {};
-            int64_t rows[4];            // first cache row of each 16-key block, -1: none
-            float sv[4][2];
+            const int k0 = tile * TILE;
+            const uint32_t here = live[0];
+            if (!ptx::mbar_wait(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag)) break;
+            const uint8_t *st = ring + slot * STAGE;
+            const uint16_t *sks = reinterpret_cast<const uint16_t *>(st + TILE * D), *svs = sks + TILE;
+            float s[NB][NT][4] = {};
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-                const int j0 = k0 + 16 * blk;
-                rows[blk] = -1;
-                sv[blk][0] = sv[blk][1] = 0.0f;
-                if (j0 < rq.len) {
-                    const int id = table[j0 >> a.c.page_shift];
-                    if (id >= 0 && id < a.c.num_pages)
-                        rows[blk] = ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) +
-                                    (j0 & ((1 << a.c.page_shift) - 1));
-                    else if (lane == 0) page_error();
-                }
-                uint32_t ka[NW] = {}, kb[NW] = {};
-                float sk[2] = {0.0f, 0.0f};
-                if (rows[blk] >= 0) {
-                    const int64_t ra = rows[blk] + sigma(g), rbw = ra + 8;
-                    sk[0] = frag::bf16_f32(a.c.ks[ra]);
-                    sk[1] = frag::bf16_f32(a.c.ks[rbw]);
-                    sv[blk][0] = frag::bf16_f32(a.c.vs[ra]);
-                    sv[blk][1] = frag::bf16_f32(a.c.vs[rbw]);
-                    const uint8_t *pa = a.c.kc + ra * (D / 2), *pb = a.c.kc + rbw * (D / 2);
-                    if constexpr (D == 64) {
-                        *reinterpret_cast<uint2 *>(ka) = *reinterpret_cast<const uint2 *>(pa + 8 * t4);
-                        *reinterpret_cast<uint2 *>(kb) = *reinterpret_cast<const uint2 *>(pb + 8 * t4);
-                    } else {
+            for (int blk = 0; blk < NB; ++blk) {
+                const int j0 = k0 + 16 * blk, ra = 16 * blk + sigma(g);
+                const uint8_t *pa = st + ra * (D / 2), *pb = pa + 8 * (D / 2);
+                uint32_t ka[NW], kb[NW];
+                if constexpr (D == 64) {
+                    *reinterpret_cast<uint2 *>(ka) = *reinterpret_cast<const uint2 *>(pa + 8 * t4);
+                    *reinterpret_cast<uint2 *>(kb) = *reinterpret_cast<const uint2 *>(pb + 8 * t4);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < NW / 4; ++i) {
-                            reinterpret_cast<uint4 *>(ka)[i] = *reinterpret_cast<const uint4 *>(pa + 64 * i + 16 * t4);
-                            reinterpret_cast<uint4 *>(kb)[i] = *reinterpret_cast<const uint4 *>(pb + 64 * i + 16 * t4);
-                        }
+                    for (int i = 0; i < NW / 4; ++i) {
+                        reinterpret_cast<uint4 *>(ka)[i] = *reinterpret_cast<const uint4 *>(pa + 64 * i + 16 * t4);
+                        reinterpret_cast<uint4 *>(kb)[i] = *reinterpret_cast<const uint4 *>(pb + 64 * i + 16 * t4);
                     }
                 }
 #pragma unroll
@@ -536,17 +594,18 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                     }
                 }
                 // scores in units of log2; hidden keys are -inf whatever they hold
+                const float ska = frag::bf16_f32(sks[ra]), skb = frag::bf16_f32(sks[ra + 8]);
                 const int ja = j0 + sigma(g), jb = ja + 8;
-                const bool all = rows[blk] >= 0 && j0 + 15 <= least;
+                const bool there = (here >> blk) & 1, all = there && j0 + 15 <= least;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        s[blk][nt][x] *= sk[0] * cs[nt][x];
-                        s[blk][nt][2 + x] *= sk[1] * cs[nt][x];
+                        s[blk][nt][x] *= ska * cs[nt][x];
+                        s[blk][nt][2 + x] *= skb * cs[nt][x];
                         if (!all) {
-                            if (rows[blk] < 0 || ja > cmax[nt][x]) s[blk][nt][x] = -INFINITY;
-                            if (rows[blk] < 0 || jb > cmax[nt][x]) s[blk][nt][2 + x] = -INFINITY;
+                            if (!there || ja > cmax[nt][x]) s[blk][nt][x] = -INFINITY;
+                            if (!there || jb > cmax[nt][x]) s[blk][nt][2 + x] = -INFINITY;
                         }
                     }
             }
@@ -559,21 +618,23 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 for (int x = 0; x < 2; ++x) {
                     float top = m[nt][x];
 #pragma unroll
-                    for (int blk = 0; blk < 4; ++blk) top = fmaxf(top, fmaxf(s[blk][nt][x], s[blk][nt][2 + x]));
+                    for (int blk = 0; blk < NB; ++blk) top = fmaxf(top, fmaxf(s[blk][nt][x], s[blk][nt][2 + x]));
                     for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
                     const float safe = top == -INFINITY ? 0.0f : top;
-                    mul[nt][x] = exp2f(m[nt][x] - safe);
+                    mul[nt][x] = ex2(m[nt][x] - safe);
                     turn |= top != m[nt][x];
                     m[nt][x] = top;
                     l[nt][x] *= mul[nt][x];
 #pragma unroll
-                    for (int blk = 0; blk < 4; ++blk)
+                    for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
                         for (int y = 0; y < 4; y += 2) {
-                            const float p = exp2f(s[blk][nt][y + x] - safe);
+                            const float p = ex2(s[blk][nt][y + x] - safe);
                             l[nt][x] += p;
                             // a hidden key's scale may be anything
-                            s[blk][nt][y + x] = s[blk][nt][y + x] == -INFINITY ? 0.0f : p * sv[blk][y >> 1];
+                            s[blk][nt][y + x] = s[blk][nt][y + x] == -INFINITY
+                                                    ? 0.0f
+                                                    : p * frag::bf16_f32(svs[16 * blk + sigma(g) + 4 * y]);
                         }
                 }
             if (__any_sync(0xFFFFFFFFu, turn)) {
@@ -586,8 +647,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             }
             // ---- O^T += V^T P^T
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-                if (rows[blk] < 0) continue;
+            for (int blk = 0; blk < NB; ++blk) {
                 uint32_t p0[NT], p1[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -598,8 +658,8 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 uint32_t v[4][VW];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = sigma(2 * t4 + (i & 1)) + 8 * (i >> 1);
-                    const uint8_t *p = a.c.vc + (rows[blk] + key) * (D / 2) + 4 * VW * g;
+                    const int key = 16 * blk + sigma(2 * t4 + (i & 1)) + 8 * (i >> 1);
+                    const uint8_t *p = st + TILE * (D / 2) + key * (D / 2) + 4 * VW * g;
                     if constexpr (VW == 1) v[i][0] = *reinterpret_cast<const uint32_t *>(p);
                     else if constexpr (VW == 2) *reinterpret_cast<uint2 *>(v[i]) = *reinterpret_cast<const uint2 *>(p);
                     else *reinterpret_cast<uint4 *>(v[i]) = *reinterpret_cast<const uint4 *>(p);
@@ -619,9 +679,19 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                             frag::mma_bf16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p0[nt], p1[nt]);
                 }
             }
+            __syncwarp();               // the slot has been read
+#pragma unroll
+            for (int i = 0; i + 1 < DEPTH; ++i) live[i] = live[i + 1];
+            const int far = tile + DEPTH * kAttnWarps;
+            if (far < tile1) live[DEPTH - 1] = request(far, slot);
+            if (++slot == DEPTH) {
+                slot = 0;
+                parity ^= 1;
+            }
         }
 
         // ---- join the warps
+        __syncthreads();                // every ring is drained
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -653,7 +723,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             float x[16] = {}, sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = exp2f(wm[w][r] - safe);
+                const float f = ex2(wm[w][r] - safe);
                 sum += f * wl[w][r];
                 const float4 *src = reinterpret_cast<const float4 *>(osum + (w * ROWS + r) * PITCH + 16 * part);
 #pragma unroll
@@ -677,6 +747,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
         }
+        ptx::fence_proxy_async_smem();  // these reads and writes come before the next copies into the rings
         if (!whole && seg_u0 >= u0 && tid == 0)
             a.desc[blockIdx.x] = make_int4(static_cast<int>((seg_u1 - 1) / share), b, h, rb);
         u = seg_u0 + tile1;
@@ -691,7 +762,7 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
     ptx::grid_dependency_wait();
     const int4 d = a.desc[blockIdx.x];
     if (d.x < 0) return;
-    const Request rq = request_of<ROWS>(a, d.y);
+    const Request rq = request_of<D, ROWS>(a, d.y);
     for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
         const int i = i0 + static_cast<int>(threadIdx.x);
         const int r = min(i / LANES, ROWS - 1), part = i % LANES;
@@ -701,7 +772,7 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
             const float mc = p[2 * r], lc = p[2 * r + 1];
             const float next = fmaxf(top, mc);
             const float safe = next == -INFINITY ? 0.0f : next;
-            const float fo = exp2f(top - safe), fn = exp2f(mc - safe);
+            const float fo = ex2(top - safe), fn = ex2(mc - safe);
             top = next;
             sum = sum * fo + lc * fn;
             const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
@@ -720,7 +791,7 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
 
 template <int D, int NT>
 constexpr int attn_smem() {
-    return NT * (D / 32) * 512 + kAttnWarps * 8 * NT * (D + 4) * 4;
+    return NT * (D / 32) * 512 + kAttnWarps * ring_depth(D) * tile_keys(D) * (D + 4);
 }
 
 }  // namespace kv4
@@ -799,9 +870,9 @@ int row_tiles(int64_t T, int64_t B, int G, int D) {
 }
 
 // CTAs that can have work at most, from what the host knows.
-int64_t attn_ctas(int64_t T, int64_t B, int G, int kv_heads, int NT, int64_t max_keys) {
+int64_t attn_ctas(int64_t T, int64_t B, int G, int kv_heads, int NT, int D, int64_t max_keys) {
     const int64_t blocks = (T * G + 8 * NT - 1) / (8 * NT) + B;
-    const int64_t tiles = (max_keys + kTile - 1) / kTile;
+    const int64_t tiles = (max_keys + tile_keys(D) - 1) / tile_keys(D);
     // beyond kMaxCtas the product is not needed, and could overflow
     if (blocks > 8 * kMaxCtas || tiles > 8 * kMaxCtas) return kMaxCtas;
     const int64_t n = (blocks * (tiles > 0 ? tiles : 1) * kv_heads + kMinUnits - 1) / kMinUnits;
@@ -908,7 +979,7 @@ size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int
                                             int head_dim, int64_t max_keys) {
     if (!attn_shape_ok(T, B, heads, kv_heads, head_dim, max_keys) || T == 0 || B == 0) return 0;
     const int G = heads / kv_heads, NT = row_tiles(T, B, G, head_dim);
-    const size_t ctas = static_cast<size_t>(attn_ctas(T, B, G, kv_heads, NT, max_keys));
+    const size_t ctas = static_cast<size_t>(attn_ctas(T, B, G, kv_heads, NT, head_dim, max_keys));
     return host::round256(ctas * sizeof(int4)) + ctas * 2 * 8 * NT * (head_dim + 2) * sizeof(float);
 }
 
@@ -937,7 +1008,7 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
                                             cache->k_scales, cache->v_codes, cache->v_scales})) != CONVROT_OK)
         return st;
     const int G = heads / cache->kv_heads, NT = row_tiles(T, B, G, D);
-    const int64_t ctas = attn_ctas(T, B, G, cache->kv_heads, NT, max_pages * cache->page);
+    const int64_t ctas = attn_ctas(T, B, G, cache->kv_heads, NT, D, max_pages * cache->page);
     AttnArgs a{device_cache(cache), static_cast<const uint16_t *>(q_bf16), ldq, T, G, block_table, max_pages,
                seq_lens, cu_q, static_cast<int>(B), scale * 1.4426950408889634f, static_cast<int4 *>(workspace),
                reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(ctas * sizeof(int4))),
