@@ -19,31 +19,27 @@
 namespace frag {
 
 // Codes of one 32-bit word (8 codes, low nibble first) as f16 pairs
-// (c0, c4), (c1, c5), (c2, c6), (c3, c7), exact.  A nibble XOR 8 is code + 8;
-// in the low mantissa bits of 0x6400 (1024.0, spacing 1) it reads
-// 1024 + code + 8, and one bit group further up 1024 + 16 (code + 8): one
-// subtraction, or one FMA with 1/16, leaves the code.
-__device__ __forceinline__ void widen_f16(uint32_t w, uint32_t (&o)[4]) {
+// (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7), each code offset by 8 and all
+// times 2^-24.  A nibble XOR 8 is u = code + 8, and an f16 whose bits are a
+// small whole number u is the subnormal u 2^-24, exactly, which the matrix
+// product takes at its full value: one operation a pair and one shift a word,
+// against two a pair for a conversion that removes the offset.  The second of
+// two nibbles stays where it is and counts 16 times.  Callers put the factors
+// into the other operand or the result and take 8 times the other operand's
+// sum off.
+constexpr float kCodeUnit = 1.0f / 16777216.0f;   // 2^-24
+
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4]) {
     const uint32_t w8 = w >> 8;
-    const __half2 lo = __halves2half2(__ushort_as_half(0xE408), __ushort_as_half(0xE408));   // -1032
-    const __half2 sc = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));   // 1 / 16
-    const __half2 hi = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));   // -72
-    uint32_t a = (w & 0x000F000Fu) ^ 0x64086408u;
-    uint32_t b = (w & 0x00F000F0u) ^ 0x64806480u;
-    uint32_t c = (w8 & 0x000F000Fu) ^ 0x64086408u;
-    uint32_t d = (w8 & 0x00F000F0u) ^ 0x64806480u;
-    __half2 ha = __hadd2(*reinterpret_cast<__half2 *>(&a), lo);
-    __half2 hb = __hfma2(*reinterpret_cast<__half2 *>(&b), sc, hi);
-    __half2 hc = __hadd2(*reinterpret_cast<__half2 *>(&c), lo);
-    __half2 hd = __hfma2(*reinterpret_cast<__half2 *>(&d), sc, hi);
-    o[0] = *reinterpret_cast<uint32_t *>(&ha);
-    o[1] = *reinterpret_cast<uint32_t *>(&hb);
-    o[2] = *reinterpret_cast<uint32_t *>(&hc);
-    o[3] = *reinterpret_cast<uint32_t *>(&hd);
+    o[0] = (w & 0x000F000Fu) ^ 0x00080008u;
+    o[1] = (w & 0x00F000F0u) ^ 0x00800080u;
+    o[2] = (w8 & 0x000F000Fu) ^ 0x00080008u;
+    o[3] = (w8 & 0x00F000F0u) ^ 0x00800080u;
 }
 
-// The same as bf16 pairs: 0x4300 is 128.0 with spacing 1, so only the low
-// nibble of each half has room and the word is shifted between pairs.
+// The codes as exact bf16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7): 0x4300
+// is 128.0 with spacing 1, so 128 + code + 8 is one XOR away and one
+// subtraction leaves the code.
 __device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t (&o)[4]) {
     const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xC308),
                                                   __ushort_as_bfloat16(0xC308));             // -136

@@ -265,19 +265,27 @@ read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *_
 // ------------------------------------------------------------------ attention
 // Per request and shared head, the rows are the queries of the heads that
 // share it times the new tokens, in blocks of ROWS = 8 NT; the keys go by in
-// tiles of 64, one tile a warp at a time, with the running maximum and sum of
-// a softmax in fp32:
-//   S^T (64 keys x ROWS) = K (codes, f16) Q^T          mma, A = codes
-//   P = exp2(S s_k - max);  O^T (D x ROWS) += V^T (codes, bf16) (P s_v)^T
+// tiles of 64 (32 with D = 256), one tile a warp at a time, with the running
+// maximum and sum of a softmax in fp32:
+//   S^T (keys x ROWS) = K (codes) Q^T           mma m16n8k16, A = codes
+//   P = exp2(S s_k - max);  O^T (D x ROWS) += V^T (codes) (P s_v)^T
 // Codes are the A operand of both products (16 rows an instruction against 8
 // of the B side), so one instruction takes 256 codes.  K's scale goes into the
 // scores and V's into P, both in fp32.
 //
+// Instruction issue is what bounds the loop, so the codes are not converted:
+// they go in as f16 subnormals offset by 8 (frag::codes_f16).  The offset's
+// part of a score, -8 times the sum of the query's values, is where the
+// product's accumulator starts; that of the outputs, -8 times the sum of the
+// weights, comes out of one more product with a matrix of ones and is taken
+// off before each tile.
+//
 // The queries are f16, scaled by a power of two that puts the row's largest
-// value at 2^14 .. 2^15 and taken out again in fp32: their rounding is
-// 2^-12 relative, a power below bf16's by eight.  P s_v is rounded to bf16
-// (2^-9 relative, independent from key to key): its range is that of s_v,
-// which f16 could not hold.
+// value at 2^14 .. 2^15 and taken out again in fp32: their rounding is 2^-11
+// relative, an eighth of bf16's.  P s_v is f16 too, relative to the
+// largest exponent of s_v so far (powers of two; outputs are rescaled when it
+// grows, as they are when the maximum does): 2^-11 relative for weights down
+// to 2^-28 of the largest.
 //
 // Which keys of a 16-key block sit in which row of the product is free as
 // long as both products agree.  Row r holds key sigma(r), chosen so that both
@@ -303,6 +311,7 @@ constexpr int kMaxCtas = 592;
 __host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
 __host__ __device__ constexpr int ring_depth(int D) { return D == 64 ? 3 : 2; }
 constexpr int kMinUnits = kAttnWarps;   // at least one tile a warp
+constexpr uint32_t kLeastExponent = 15;   // of a reference scale, so that 2^14 over it is a float
 
 struct AttnArgs {
     Cache c;
@@ -388,9 +397,9 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     static_assert(kAttnWarps * ROWS * PITCH * 4 <= kAttnWarps * DEPTH * STAGE, "outputs fit the rings");
     __shared__ uint64_t bars[kAttnWarps][DEPTH];
     __shared__ int abort_flag;
-    __shared__ float qs[ROWS];
+    __shared__ float qs[ROWS], qoff[ROWS];
     __shared__ int qmax[ROWS];
-    __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS];
+    __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS], wunit[kAttnWarps];
     __shared__ long long scan[kAttnWarps];
     __shared__ long long start_unit;
     __shared__ int start_b;
@@ -517,9 +526,18 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             // 2^(14 - floor(log2 amax)), its exponent kept in range
             const int e = min(254, 127 + 14 - (static_cast<int>(amax >> 23) - 127));
             const float f = amax ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
+            // two values for the codes of one pair, those of second nibbles a
+            // sixteenth; their sum (as rounded) goes into the offset
+            float sum = 0.0f;
+            auto pack = [&](float lo, float hi, float div) {
+                const uint32_t w = frag::pack_f16(lo / div, hi / div);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                sum += div * (v.x + v.y);
+                return w;
+            };
             if (r < ROWS) {
                 if (part == 0) {
-                    qs[r] = amax ? a.scale * frag::norm_of(a.c.group) * __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 0.0f;
+                    qs[r] = amax ? a.scale * (frag::norm_of(a.c.group) / frag::kCodeUnit) * __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 0.0f;
                     qmax[r] = rq.len - rq.nq + min(qi, rq.nq - 1);   // rows past the last query are not stored
                 }
 #pragma unroll
@@ -528,16 +546,21 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                     const int tq = D == 64 ? d / 16 : (d % 128) / 32;
                     const int j = D == 64 ? (d % 16) / 8 : 4 * (d / 128) + (d % 32) / 8;
                     const float *y = x + 8 * half;
-                    qf[((r >> 3) * NW + j) * 32 + (r & 7) * 4 + tq] =
-                        make_uint4(frag::pack_f16(y[0] * f, y[4] * f), frag::pack_f16(y[1] * f, y[5] * f),
-                                   frag::pack_f16(y[2] * f, y[6] * f), frag::pack_f16(y[3] * f, y[7] * f));
+                    uint4 w;
+                    w.x = pack(y[0] * f, y[4] * f, 1.0f);
+                    w.y = pack(y[1] * f, y[5] * f, 16.0f);
+                    w.z = pack(y[2] * f, y[6] * f, 1.0f);
+                    w.w = pack(y[3] * f, y[7] * f, 16.0f);
+                    qf[((r >> 3) * NW + j) * 32 + (r & 7) * 4 + tq] = w;
                 }
             }
+            for (int k = 1; k < LANES; k <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+            if (r < ROWS && part == 0) qoff[r] = -8.0f * frag::kCodeUnit * sum;
         }
         __syncthreads();
 
         // thread's columns: queries 8 nt + 2 t4 and + 1
-        float cs[NT][2];
+        float cs[NT][2], off[NT][2];
         int cmax[NT][2];
         int least = 0x7FFFFFFF;
 #pragma unroll
@@ -545,13 +568,20 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 cs[nt][x] = qs[8 * nt + 2 * t4 + x];
+                off[nt][x] = qoff[8 * nt + 2 * t4 + x];
                 cmax[nt][x] = qmax[8 * nt + 2 * t4 + x];
                 least = min(least, cmax[nt][x]);
             }
         for (int s = 1; s < 4; s <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, s));
+        // the fragments stay in registers where there is room
+        uint4 qreg[NT == 1 ? NW : 1];
+        if constexpr (NT == 1)
+#pragma unroll
+            for (int j = 0; j < NW; ++j) qreg[j] = qf[j * 32 + lane];
 
         float o[MT][NT][4] = {};
         float m[NT][2], l[NT][2];
+        uint32_t ref = kLeastExponent;  // the values' scales are taken relative to 2^(ref - 127 - 14)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -559,16 +589,19 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 m[nt][x] = -INFINITY;
                 l[nt][x] = 0.0f;
             }
+
         for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
             const int k0 = tile * TILE;
             const uint32_t here = live[0];
+            // every query sees every key of the tile
+            const bool all = here == (1u << NB) - 1 && k0 + TILE - 1 <= least;
             if (!ptx::mbar_wait(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag)) break;
             const uint8_t *st = ring + slot * STAGE;
             const uint16_t *sks = reinterpret_cast<const uint16_t *>(st + TILE * D), *svs = sks + TILE;
-            float s[NB][NT][4] = {};
+            float s[NB][NT][4];
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
-                const int j0 = k0 + 16 * blk, ra = 16 * blk + sigma(g);
+                const int ra = 16 * blk + sigma(g);
                 const uint8_t *pa = st + ra * (D / 2), *pb = pa + 8 * (D / 2);
                 uint32_t ka[NW], kb[NW];
                 if constexpr (D == 64) {
@@ -582,43 +615,71 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                     }
                 }
 #pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[blk][nt][x] = off[nt][x & 1];
+#pragma unroll
                 for (int j = 0; j < NW; ++j) {
                     uint32_t wa[4], wb[4];
-                    frag::widen_f16(ka[j], wa);
-                    frag::widen_f16(kb[j], wb);
+                    frag::codes_f16(ka[j], wa);
+                    frag::codes_f16(kb[j], wb);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 q = qf[(nt * NW + j) * 32 + lane];
+                        const uint4 q = NT == 1 ? qreg[j] : qf[(nt * NW + j) * 32 + lane];
                         frag::mma_f16(s[blk][nt], wa[0], wb[0], wa[1], wb[1], q.x, q.y);
                         frag::mma_f16(s[blk][nt], wa[2], wb[2], wa[3], wb[3], q.z, q.w);
                     }
                 }
-                // scores in units of log2; hidden keys are -inf whatever they hold
+                // scores in units of log2
                 const float ska = frag::bf16_f32(sks[ra]), skb = frag::bf16_f32(sks[ra + 8]);
-                const int ja = j0 + sigma(g), jb = ja + 8;
-                const bool there = (here >> blk) & 1, all = there && j0 + 15 <= least;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         s[blk][nt][x] *= ska * cs[nt][x];
                         s[blk][nt][2 + x] *= skb * cs[nt][x];
-                        if (!all) {
-                            if (!there || ja > cmax[nt][x]) s[blk][nt][x] = -INFINITY;
-                            if (!there || jb > cmax[nt][x]) s[blk][nt][2 + x] = -INFINITY;
-                        }
                     }
             }
+            if (!all) {
+                // hidden keys are -inf whatever they hold
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk) {
+                    const int ja = k0 + 16 * blk + sigma(g);
+                    const bool there = (here >> blk) & 1;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) s[blk][nt][x] = -INFINITY;
+                }
+            }
+            // the largest exponent of the values' scales so far; hidden and
+            // infinite ones do not count
+            uint32_t top_bits = 0;
+            if (2 * lane < TILE) {
+                const uint32_t two = reinterpret_cast<const uint32_t *>(svs)[lane];
+                const bool there = (here >> (lane >> 3)) & 1;
+                const uint32_t lo = two & 0xFFFFu, hi = two >> 16;
+                if (there && k0 + 2 * lane < rq.len && lo < 0x7F80u) top_bits = lo;
+                if (there && k0 + 2 * lane + 1 < rq.len && hi < 0x7F80u) top_bits = max(top_bits, hi);
+            }
+            const uint32_t exponent = __reduce_max_sync(0xFFFFFFFFu, top_bits) >> 7;
+            float shift = 1.0f;
+            bool turn = exponent > ref;
+            if (turn) {
+                shift = exponent - ref < 127 ? __uint_as_float((127 - (exponent - ref)) << 23) : 0.0f;
+                ref = exponent;
+            }
+            const float unit = __uint_as_float((127 + 14 + 127 - ref) << 23);   // 2^14 over the reference
             // ---- running maximum and sum
             float mul[NT][2];
-            bool turn = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float top = m[nt][x];
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) top = fmaxf(top, fmaxf(s[blk][nt][x], s[blk][nt][2 + x]));
+                    for (int blk = 0; blk < NB; ++blk) top = prep::max3(top, s[blk][nt][x], s[blk][nt][2 + x]);
                     for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
                     const float safe = top == -INFINITY ? 0.0f : top;
                     mul[nt][x] = ex2(m[nt][x] - safe);
@@ -631,12 +692,34 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                         for (int y = 0; y < 4; y += 2) {
                             const float p = ex2(s[blk][nt][y + x] - safe);
                             l[nt][x] += p;
-                            // a hidden key's scale may be anything
-                            s[blk][nt][y + x] = s[blk][nt][y + x] == -INFINITY
-                                                    ? 0.0f
-                                                    : p * frag::bf16_f32(svs[16 * blk + sigma(g) + 4 * y]);
+                            s[blk][nt][y + x] = p;
                         }
+                    mul[nt][x] *= shift;
                 }
+            // ---- weights of the values, as f16 fragments, and their sums
+            uint32_t p0[NB][NT], p1[NB][NT];
+            float psum[NT][4] = {};
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk) {
+                const float sva = unit * frag::bf16_f32(svs[16 * blk + sigma(g)]);
+                const float svb = unit * frag::bf16_f32(svs[16 * blk + sigma(g) + 8]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] = s[blk][nt][x] * (x < 2 ? sva : svb);
+                    if (!all) {         // a hidden key's scale may be anything
+                        const int ja = k0 + 16 * blk + sigma(g);
+                        const bool there = (here >> blk) & 1;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) w[x] = 0.0f;
+                    }
+                    p0[blk][nt] = frag::transpose8x8(frag::pack_f16(w[0], w[1]));
+                    p1[blk][nt] = frag::transpose8x8(frag::pack_f16(w[2], w[3]));
+                    frag::mma_f16(psum[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p0[blk][nt], p1[blk][nt]);
+                }
+            }
             if (__any_sync(0xFFFFFFFFu, turn)) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
@@ -645,15 +728,20 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) o[i][nt][x] *= mul[nt][x & 1];
             }
+            // the codes' offset of 8, taken off tile by tile so that it never
+            // grows far beyond the sums it is part of
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float one[2] = {-8.0f * frag::kCodeUnit * psum[nt][0], -8.0f * frag::kCodeUnit * psum[nt][1]};
+                const float second[2] = {16.0f * one[0], 16.0f * one[1]};
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[i][nt][x] += (i & 1) ? second[x & 1] : one[x & 1];
+            }
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
-                uint32_t p0[NT], p1[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    p0[nt] = frag::transpose8x8(frag::pack_bf16(s[blk][nt][0], s[blk][nt][1]));
-                    p1[nt] = frag::transpose8x8(frag::pack_bf16(s[blk][nt][2], s[blk][nt][3]));
-                }
                 // columns 2 t4, 2 t4 + 1 of the product are the keys sigma of those
                 uint32_t v[4][VW];
 #pragma unroll
@@ -668,15 +756,15 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 for (int w = 0; w < VW; ++w) {
                     // halves of two keys side by side: codes 0-3, then 4-7
                     uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
-                    frag::widen_bf16(__byte_perm(v[0][w], v[1][w], 0x5410), lo0);
-                    frag::widen_bf16(__byte_perm(v[0][w], v[1][w], 0x7632), hi0);
-                    frag::widen_bf16(__byte_perm(v[2][w], v[3][w], 0x5410), lo1);
-                    frag::widen_bf16(__byte_perm(v[2][w], v[3][w], 0x7632), hi1);
+                    frag::codes_f16(__byte_perm(v[0][w], v[1][w], 0x5410), lo0);
+                    frag::codes_f16(__byte_perm(v[0][w], v[1][w], 0x7632), hi0);
+                    frag::codes_f16(__byte_perm(v[2][w], v[3][w], 0x5410), lo1);
+                    frag::codes_f16(__byte_perm(v[2][w], v[3][w], 0x7632), hi1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            frag::mma_bf16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p0[nt], p1[nt]);
+                            frag::mma_f16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p0[blk][nt], p1[blk][nt]);
                 }
             }
             __syncwarp();               // the slot has been read
@@ -702,6 +790,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                     wl[warp][8 * nt + 2 * t4 + x] = l[nt][x];
                 }
             }
+        if (lane == 0) wunit[warp] = __uint_as_float((ref - 14) << 23);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -709,7 +798,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     osum[(warp * ROWS + 8 * nt + 2 * t4 + (x & 1)) * PITCH + (D / 8) * g + 8 * (i >> 2) + (i & 3) +
-                         4 * (x >> 1)] = o[i][nt][x];
+                         4 * (x >> 1)] = o[i][nt][x] * ((i & 1) ? 1.0f / (16.0f * frag::kCodeUnit) : 1.0f / frag::kCodeUnit);
         __syncthreads();
         const bool whole = seg_u0 >= u0 && seg_u1 <= u1;
         float *part_out = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (seg_u0 >= u0 ? 1 : 0)) * (ROWS * (D + 2));
@@ -723,8 +812,8 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             float x[16] = {}, sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = ex2(wm[w][r] - safe);
-                sum += f * wl[w][r];
+                const float e = ex2(wm[w][r] - safe), f = e * wunit[w];
+                sum += e * wl[w][r];
                 const float4 *src = reinterpret_cast<const float4 *>(osum + (w * ROWS + r) * PITCH + 16 * part);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

@@ -59,6 +59,11 @@ def cache_rows(codes, scales, table, n, h):
     return c * scales[ids, h].reshape(-1)[:n].double()[:, None]
 
 
+def ks_rows(scales, table, n, h):
+    page = scales.shape[2]
+    return scales[table[:-(-n // page)].long(), h].reshape(-1)[:n].double()
+
+
 def attention(q, cache, table, lens, cu_q, scale, group, dead=()):
     """(out, tolerance norm, terms) float64: out [T, heads, D]; per row an
     allowance for the kernel's roundings as derived in test_gpu_kv4.py.
@@ -92,15 +97,24 @@ def attention(q, cache, table, lens, cu_q, scale, group, dead=()):
                     s = kk @ qr * scale
                     p = torch.softmax(s, 0)
                     out[a + i, hq] = rotate(p @ vv, group)
-                    # scores: f16 queries (2^-12 of each value, 2^-39 of the
-                    # row's largest), fp32 rotation and sums (2^-17 of the terms)
-                    l1 = kk.abs() @ (qr.abs() * (2.0 ** -12 + 2.0 ** -17) + qr.abs().max() * (2.0 ** -39 + 1e-5)) * abs(scale)
+                    # scores: f16 queries (2^-11 of each value, 2^-34 of the
+                    # row's largest), fp32 rotation and sums (2^-17 of the terms,
+                    # and of 8 s_k sum |q|, the offset that the codes carry:
+                    # up to 16 steps, each off by at most an ulp, 2^-23)
+                    l1 = kk.abs() @ (qr.abs() * (2.0 ** -11 + 2.0 ** -17) + qr.abs().max() * (2.0 ** -34 + 1e-5)) * abs(scale)
+                    l1 = l1 + ks_rows(ks, row, n, h)[seen] * (8 * qr.abs().sum() * 16 * 2.0 ** -23 * abs(scale))
                     # and the maximum taken off in fp32 (2^-24 of the score), exp2f 2 ulp
                     ds = float((l1 + s.abs() * 2.0 ** -22).max()) + 2.0 ** -22
                     # weights: both the numerator and the sum move by ds; P s_v in
-                    # bf16 (2^-9 of a value is half a step at most 2^-8)
-                    e = float(np.expm1(2 * ds)) + 2.0 ** -8 + 2.0 ** -16
+                    # f16 (2^-11); fp32 sums 2^-16
+                    e = float(np.expm1(2 * ds)) + 2.0 ** -11 + 2.0 ** -16
                     allow[a + i, hq] = e * (p @ vv.abs()).norm() + 2.0 ** -8 * out[a + i, hq].norm()
+                    # the offset of the values' codes comes and goes in every
+                    # tile: 8 sum p s_v, off by an ulp (2^-23) in each of five
+                    # steps, and weights below the f16 range (2^-34 of the
+                    # largest scale each), in each of D values
+                    sv = ks_rows(vs, row, n, h)[seen]
+                    allow[a + i, hq] += D ** 0.5 * (8 * 5 * 2.0 ** -23 * float(p @ sv) + 7 * 2.0 ** -34 * float(sv.max()) * len(sv))
     return out, allow
 
 
