@@ -29,12 +29,31 @@ namespace frag {
 // sum off.
 constexpr float kCodeUnit = 1.0f / 16777216.0f;   // 2^-24
 
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4]) {
+// The masks are values that the compiler cannot see: as immediates the AND and
+// the XOR, one three-input operation between registers, become two.
+struct CodeMasks {
+    uint32_t low, low8, high, high8;
+    __device__ __forceinline__ CodeMasks() {
+        const uint32_t z = gridDim.z;   // 1
+        low = 0x000F000Eu + z;
+        low8 = 0x00080007u + z;
+        high = 0x00F000EFu + z;
+        high8 = 0x0080007Fu + z;
+    }
+};
+
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(m), "r"(x));   // (w & m) ^ x
+    return r;
+}
+
+__device__ __forceinline__ void codes_f16(const CodeMasks &k, uint32_t w, uint32_t (&o)[4]) {
     const uint32_t w8 = w >> 8;
-    o[0] = (w & 0x000F000Fu) ^ 0x00080008u;
-    o[1] = (w & 0x00F000F0u) ^ 0x00800080u;
-    o[2] = (w8 & 0x000F000Fu) ^ 0x00080008u;
-    o[3] = (w8 & 0x00F000F0u) ^ 0x00800080u;
+    o[0] = and_xor(w, k.low, k.low8);
+    o[1] = and_xor(w, k.high, k.high8);
+    o[2] = and_xor(w8, k.low, k.low8);
+    o[3] = and_xor(w8, k.high, k.high8);
 }
 
 // The codes as exact bf16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7): 0x4300

@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     uint32_t parity = 0;                // of the slot's next completion
     const uint8_t *ring = rings + warp * (DEPTH * STAGE);
     const uint32_t ring_s = ptx::smem_u32(ring);
+    const frag::CodeMasks masks;
     const int piece_shift = min(a.c.page_shift, TILE == 64 ? 6 : 5);   // keys of a tile in one page
 
     for (long long u = u0; u < u1;) {
@@ -621,8 +622,8 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 #pragma unroll
                 for (int j = 0; j < NW; ++j) {
                     uint32_t wa[4], wb[4];
-                    frag::codes_f16(ka[j], wa);
-                    frag::codes_f16(kb[j], wb);
+                    frag::codes_f16(masks, ka[j], wa);
+                    frag::codes_f16(masks, kb[j], wb);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const uint4 q = NT == 1 ? qreg[j] : qf[(nt * NW + j) * 32 + lane];
@@ -756,10 +757,10 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 for (int w = 0; w < VW; ++w) {
                     // halves of two keys side by side: codes 0-3, then 4-7
                     uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
-                    frag::codes_f16(__byte_perm(v[0][w], v[1][w], 0x5410), lo0);
-                    frag::codes_f16(__byte_perm(v[0][w], v[1][w], 0x7632), hi0);
-                    frag::codes_f16(__byte_perm(v[2][w], v[3][w], 0x5410), lo1);
-                    frag::codes_f16(__byte_perm(v[2][w], v[3][w], 0x7632), hi1);
+                    frag::codes_f16(masks, __byte_perm(v[0][w], v[1][w], 0x5410), lo0);
+                    frag::codes_f16(masks, __byte_perm(v[0][w], v[1][w], 0x7632), hi0);
+                    frag::codes_f16(masks, __byte_perm(v[2][w], v[3][w], 0x5410), lo1);
+                    frag::codes_f16(masks, __byte_perm(v[2][w], v[3][w], 0x7632), hi1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
