@@ -18,8 +18,15 @@
 
 namespace frag {
 
-// Codes of one 32-bit word (8 codes, low nibble first) as f16 pairs
-// (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7), each code offset by 8 and all
+// Codes of one 32-bit word (8 codes, low nibble first) as int8: 16 times the
+// odd codes and 16 times the even codes (a nibble at the top of a byte is the
+// signed code times 16).
+__device__ __forceinline__ void codes_s8(uint32_t w, uint32_t &odd, uint32_t &even) {
+    odd = w & 0xF0F0F0F0u;
+    even = (w * 16u) & 0xF0F0F0F0u;
+}
+
+// Codes of one 32-bit word as f16 pairs (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7), each code offset by 8 and all
 // times 2^-24.  A nibble XOR 8 is u = code + 8, and an f16 whose bits are a
 // small whole number u is the subnormal u 2^-24, exactly, which the matrix
 // product takes at its full value: one operation a pair and one shift a word,
@@ -73,7 +80,7 @@ __device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t (&o)[4]) {
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -82,17 +89,26 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D (16 x 8, int32) += A (16 x 32, int8) B (32 x 8, int8), exact.
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The transpose of an 8 x 8 tile of 16-bit values held one row per 4 lanes.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 

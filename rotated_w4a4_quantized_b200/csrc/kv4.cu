@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/convrot_kv4.h"
 #include "frag.cuh"
 #include "host.cuh"
@@ -264,37 +266,41 @@ read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *_
 
 // ------------------------------------------------------------------ attention
 // Per request and shared head, the rows are the queries of the heads that
-// share it times the new tokens, in blocks of ROWS = 8 NT; the keys go by in
-// tiles of 64 (32 with D = 256), one tile a warp at a time, with the running
-// maximum and sum of a softmax in fp32:
-//   S^T (keys x ROWS) = K (codes) Q^T           mma m16n8k16, A = codes
-//   P = exp2(S s_k - max);  O^T (D x ROWS) += V^T (codes) (P s_v)^T
+// share it times the new tokens, in blocks of ROWS; the keys go by in tiles of
+// 64, one tile a warp at a time, with the running maximum and sum of a softmax
+// in fp32:
+//   S^T (keys x ROWS) = K (codes) Q^T           mma m16n8k32, int8, A = codes
+//   P = exp2(S s_k - max)
+//   O^T (D x ROWS) += V^T (codes) (P s_v)^T     mma m16n8k16, f16, A = codes
 // Codes are the A operand of both products (16 rows an instruction against 8
-// of the B side), so one instruction takes 256 codes.  K's scale goes into the
-// scores and V's into P, both in fp32.
+// of the B side).  K's scale goes into the scores and V's into P, in fp32.
 //
-// Instruction issue is what bounds the loop, so the codes are not converted:
-// they go in as f16 subnormals offset by 8 (frag::codes_f16).  The offset's
-// part of a score, -8 times the sum of the query's values, is where the
-// product's accumulator starts; that of the outputs, -8 times the sum of the
-// weights, comes out of one more product with a matrix of ones and is taken
-// off before each tile.
-//
-// The queries are f16, scaled by a power of two that puts the row's largest
-// value at 2^14 .. 2^15 and taken out again in fp32: their rounding is 2^-11
-// relative, an eighth of bf16's.  P s_v is f16 too, relative to the
-// largest exponent of s_v so far (powers of two; outputs are rescaled when it
-// grows, as they are when the maximum does): 2^-11 relative for weights down
-// to 2^-28 of the largest.
+// What bounds the loop is the integer pipe that takes the codes apart (half a
+// warp instruction a cycle), so they are converted as little as can be:
+// - K: int8, 16 times the code: two ANDs for 8 codes.  The queries are 16-bit
+//   whole numbers, the row's largest value at 32000 (off by 2^-16 of it; f16
+//   is off by 2^-11 of each value), as a high and a low byte that make two
+//   columns; the sums are exact in int32.  Up to 4 rows fill the 8 columns of
+//   one product with both bytes, and each lane then has two scores of a block
+//   instead of four.
+// - V: f16 subnormals offset by 8 (frag::codes_f16); the offset's part of the
+//   outputs, -8 times the sum of the weights, comes out of one more product
+//   with a matrix of ones and is taken off before each tile.
+// P s_v is f16 relative to the largest exponent of s_v so far (powers of two;
+// outputs are rescaled when it grows, as they are when the maximum does):
+// 2^-11 relative for weights down to 2^-28 of the largest.
 //
 // Which keys of a 16-key block sit in which row of the product is free as
 // long as both products agree.  Row r holds key sigma(r), chosen so that both
 // the 16-byte reads of K and the 4 D/64-byte reads of V spread over the banks.
 //
-// Copies.  Each warp has its own ring of stages (a tile's codes and scales,
-// about 8 KB) filled by bulk copies, one per run of keys in a page and array,
-// that complete on the warp's own barrier: no warp waits for another inside a
-// request, and an SM keeps 200 KB on the way.
+// Copies.  Each warp has its own place for a tile's keys and one for its
+// values (codes and scales, 64 (D + 4) bytes together), filled by bulk copies,
+// one per run of keys in a page, that complete on the warp's own barriers: no
+// warp waits for another inside a request.  The next tile's keys are requested
+// as soon as this one's scores are there, its values after the second product:
+// with 16 warps an SM a warp has several times the copy's latency until it
+// needs them, and registers, not bytes on the way, are what is short.
 //
 // Work.  Units of one tile for one (request, head, row block) are laid out in
 // one line; CTA c takes units [c S, (c + 1) S), so ragged lengths load the
@@ -305,11 +311,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxCtas = 592;
 
-// Keys of a tile, and tiles a warp's ring holds: about 8 KB a stage, and the
-// rings of a CTA (three fit an SM) large enough to hold the warps' outputs
-// when they are joined.
-__host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
-__host__ __device__ constexpr int ring_depth(int D) { return D == 64 ? 3 : 2; }
+constexpr int kTile = 64;               // keys
 constexpr int kMinUnits = kAttnWarps;   // at least one tile a warp
 constexpr uint32_t kLeastExponent = 15;   // of a reference scale, so that 2^14 over it is a float
 
@@ -336,7 +338,7 @@ struct Request {
 };
 
 // Request b's sizes, clamped to what its buffers hold.
-template <int D, int ROWS>
+template <int ROWS>
 __device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
     Request r;
     int64_t len = a.seq_lens[b];
@@ -348,7 +350,7 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
     r.len = static_cast<int>(len);
     r.q0 = static_cast<int>(q0);
     r.nq = q1 > q0 ? static_cast<int>(q1 - q0) : 0;
-    r.tiles = len > 0 ? (r.len - 1) / tile_keys(D) + 1 : 1;
+    r.tiles = len > 0 ? (r.len - 1) / kTile + 1 : 1;
     r.blocks = static_cast<int>((static_cast<int64_t>(r.nq) * a.G + ROWS - 1) / ROWS);
     return r;
 }
@@ -379,25 +381,27 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, 
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
-    constexpr int ROWS = 8 * NT;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) attention_kernel(AttnArgs a) {
+    constexpr bool HALF = ROWS == 4;    // the columns hold the two bytes of four queries
+    constexpr int NT = HALF ? 1 : ROWS / 8;
+    constexpr int NS = HALF ? 2 : 4;    // scores a thread, 16-key block and column tile
     constexpr int NW = D / 32;          // K words (8 codes) a thread and key
     constexpr int VW = D / 64;          // V words a thread and key
     constexpr int MT = D / 16;          // 16-row blocks of O^T
     constexpr int LANES = D / 16;
     constexpr int PITCH = D + 4;
-    constexpr int TILE = tile_keys(D), NB = TILE / 16, DEPTH = ring_depth(D);
+    constexpr int TILE = kTile, NB = TILE / 16;
     constexpr int STAGE = TILE * (D + 4);   // codes of keys, of values, scales of keys, of values
     extern __shared__ uint4 smem[];
-    // queries as B fragments: [NT][NW][32 lanes] of 16 bytes
-    uint4 *qf = smem;
-    uint8_t *rings = reinterpret_cast<uint8_t *>(smem + NT * NW * 32);
-    float *osum = reinterpret_cast<float *>(rings);   // [warps][ROWS][PITCH], when the rings are drained
-    static_assert(kAttnWarps * ROWS * PITCH * 4 <= kAttnWarps * DEPTH * STAGE, "outputs fit the rings");
-    __shared__ uint64_t bars[kAttnWarps][DEPTH];
+    // queries as B fragments, {odd, even} channels of a word: HALF: [NW][32
+    // lanes], else [NT][NW][high, low byte][32 lanes]
+    uint2 *qf = reinterpret_cast<uint2 *>(smem);
+    uint8_t *stages = reinterpret_cast<uint8_t *>(qf + (HALF ? 1 : 2 * NT) * NW * 32);
+    float *osum = reinterpret_cast<float *>(stages);  // [warps][ROWS][PITCH], once the tiles are done
+    __shared__ uint64_t bars[kAttnWarps][2];          // keys and values of a warp's tile
     __shared__ int abort_flag;
-    __shared__ float qs[ROWS], qoff[ROWS];
+    __shared__ float qs[ROWS];
     __shared__ int qmax[ROWS];
     __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS], wunit[kAttnWarps];
     __shared__ long long scan[kAttnWarps];
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     const int g = lane >> 2, t4 = lane & 3;
     if (tid == 0) abort_flag = 0;
     if (lane == 0)
-        for (int i = 0; i < DEPTH; ++i) ptx::mbar_init(ptx::smem_u32(&bars[warp][i]), 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&bars[warp][i]), 1);
     ptx::fence_mbar_init();
 
     // ---- this CTA's part of the line of units
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-        const Request r = request_of<D, ROWS>(a, b);
+        const Request r = request_of<ROWS>(a, b);
         mine += static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
     }
     long long incl = mine;
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     if (mine > 0 && before <= u0 && u0 < before + mine) {
         long long at = before;
         for (int b = b_lo; b < b_hi; ++b) {
-            const Request r = request_of<D, ROWS>(a, b);
+            const Request r = request_of<ROWS>(a, b);
             const long long n = static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
             if (u0 < at + n) {
                 start_b = b;
@@ -454,20 +458,24 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
     __syncthreads();
     int b = start_b;
     long long base = start_unit;        // first unit of request b
-    int slot = 0;
-    uint32_t parity = 0;                // of the slot's next completion
-    const uint8_t *ring = rings + warp * (DEPTH * STAGE);
-    const uint32_t ring_s = ptx::smem_u32(ring);
+    uint32_t parity = 0;                // of the warp's next tile
+    const uint8_t *st = stages + warp * STAGE;
+    const uint32_t st_s = ptx::smem_u32(st);
+    const uint32_t key_bar = ptx::smem_u32(&bars[warp][0]), value_bar = ptx::smem_u32(&bars[warp][1]);
+    const uint16_t *sks = reinterpret_cast<const uint16_t *>(st + TILE * D), *svs = sks + TILE;
     const frag::CodeMasks masks;
-    const int piece_shift = min(a.c.page_shift, TILE == 64 ? 6 : 5);   // keys of a tile in one page
+    // this thread's row in a 16-key block, of its first scores
+    const int key0 = sigma(g) + (HALF && t4 >= 2 ? 8 : 0);
+    const int col0 = HALF ? 2 * (t4 & 1) : 2 * t4;   // and its first query of a column tile
+    const int piece_shift = min(a.c.page_shift, 6);   // keys of a tile in one page
 
     for (long long u = u0; u < u1;) {
-        Request rq = request_of<D, ROWS>(a, b);
+        Request rq = request_of<ROWS>(a, b);
         long long n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
         while (u >= base + n) {
             base += n;
             if (++b >= a.B) return;     // lengths that changed under the kernel
-            rq = request_of<D, ROWS>(a, b);
+            rq = request_of<ROWS>(a, b);
             n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
         }
         const int seg = static_cast<int>((u - base) / rq.tiles);
@@ -479,40 +487,41 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 
         __syncthreads();                // the last request's shared data is done with
         const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
-        // Request a tile into a slot: lane 4 p + i copies array i of the p-th
-        // run of keys that lie in one page.  Returns a bit for each 16 keys
-        // that are there.
-        auto request = [&](int tile, int at) -> uint32_t {
-            const int p = lane >> 2, which = lane & 3, keys = 1 << piece_shift;
-            const int j0 = tile * TILE + (p << piece_shift);
-            const bool want = tile < tile1 && (p << piece_shift) < TILE && j0 < rq.len;
+        // Request a tile's keys; its values are requested once the last
+        // tile's have been read.  Lane 2 p + i copies the codes (i = 0) or the
+        // scales of the p-th run of keys that lie in one page.
+        int64_t run_row = -1;           // the run's first row in the cache
+        uint32_t live = 0, runs = 0;    // 16-key blocks that are there; lanes that copy
+        const int run = (lane >> 1) << piece_shift, run_keys = 1 << piece_shift;
+        auto copy = [&](int i) {        // keys (0) or values (1)
+            const uint32_t bar = i ? value_bar : key_bar;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (__popc(runs) >> 1) * (run_keys * (D / 2 + 2)));
+            if (run_row >= 0) {
+                if (lane & 1)
+                    bulk_load(st_s + TILE * D + i * (TILE * 2) + run * 2, (i ? a.c.vs : a.c.ks) + run_row, run_keys * 2, bar);
+                else
+                    bulk_load(st_s + i * (TILE * D / 2) + run * (D / 2), (i ? a.c.vc : a.c.kc) + run_row * (D / 2),
+                              run_keys * (D / 2), bar);
+            }
+        };
+        auto request = [&](int tile) {
+            const int j0 = tile * TILE + run;
+            const bool want = run < TILE && j0 < rq.len;
             const int id = want ? table[j0 >> a.c.page_shift] : -1;
             const bool there = want && id >= 0 && id < a.c.num_pages;
             if (want && !there) page_error();
-            const uint32_t runs = __ballot_sync(0xFFFFFFFFu, there);
-            const uint32_t bar = ptx::smem_u32(&bars[warp][at]);
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, __popc(runs & 0x11111111u) * keys * (D + 4));
-            if (there) {
-                const int64_t row = ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) +
-                                    (j0 & ((1 << a.c.page_shift) - 1));
-                const uint32_t dst = ring_s + at * STAGE;
-                if (which < 2)
-                    bulk_load(dst + which * (TILE * D / 2) + (p << piece_shift) * (D / 2),
-                              (which ? a.c.vc : a.c.kc) + row * (D / 2), keys * (D / 2), bar);
-                else
-                    bulk_load(dst + TILE * D + (which - 2) * (TILE * 2) + (p << piece_shift) * 2,
-                              (which == 3 ? a.c.vs : a.c.ks) + row, keys * 2, bar);
-            }
-            uint32_t live = 0;
+            run_row = there ? ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) +
+                                  (j0 & ((1 << a.c.page_shift) - 1))
+                            : -1;
+            runs = __ballot_sync(0xFFFFFFFFu, there);
+            live = 0;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) live |= ((runs >> (4 * ((16 * i) >> piece_shift))) & 1u) << i;
-            return live;
+            for (int i = 0; i < NB; ++i) live |= ((runs >> (2 * ((16 * i) >> piece_shift))) & 1u) << i;
+            copy(0);
         };
-        uint32_t live[DEPTH];
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-            const int at = slot + i < DEPTH ? slot + i : slot + i - DEPTH;
-            live[i] = tile0 + warp + i * kAttnWarps < tile1 ? request(tile0 + warp + i * kAttnWarps, at) : 0;
+        if (tile0 + warp < tile1) {
+            request(tile0 + warp);
+            copy(1);
         }
         // ---- queries: rotate, scale to f16, lay out as B fragments
         for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
@@ -524,21 +533,15 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             if (live) frag::load16(a.q + (static_cast<int64_t>(rq.q0) + qi) * a.ldq + static_cast<int64_t>(hd) * D + 16 * part, x);
             frag::rotate16(x, a.c.group == 256);
             const uint32_t amax = frag::absmax_bits(x, LANES);
-            // 2^(14 - floor(log2 amax)), its exponent kept in range
-            const int e = min(254, 127 + 14 - (static_cast<int>(amax >> 23) - 127));
-            const float f = amax ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
-            // two values for the codes of one pair, those of second nibbles a
-            // sixteenth; their sum (as rounded) goes into the offset
-            float sum = 0.0f;
-            auto pack = [&](float lo, float hi, float div) {
-                const uint32_t w = frag::pack_f16(lo / div, hi / div);
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-                sum += div * (v.x + v.y);
-                return w;
-            };
+            // 16-bit whole numbers, the row's largest at 32000; rows below
+            // 2^-100 count as 0, rows with a NaN or an infinity give NaN
+            const float top = __uint_as_float(amax);
+            const bool zero = amax < (27u << 23);
+            const float f = zero ? 0.0f : 32000.0f / top;
             if (r < ROWS) {
                 if (part == 0) {
-                    qs[r] = amax ? a.scale * (frag::norm_of(a.c.group) / frag::kCodeUnit) * __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 0.0f;
+                    qs[r] = zero ? 0.0f : a.scale * frag::norm_of(a.c.group) * (top / 32000.0f) / 16.0f;
+                    if (amax >= 0x7F800000u) qs[r] = __uint_as_float(0x7FC00000u);
                     qmax[r] = rq.len - rq.nq + min(qi, rq.nq - 1);   // rows past the last query are not stored
                 }
 #pragma unroll
@@ -546,37 +549,47 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                     const int d = 16 * part + 8 * half;
                     const int tq = D == 64 ? d / 16 : (d % 128) / 32;
                     const int j = D == 64 ? (d % 16) / 8 : 4 * (d / 128) + (d % 32) / 8;
-                    const float *y = x + 8 * half;
-                    uint4 w;
-                    w.x = pack(y[0] * f, y[4] * f, 1.0f);
-                    w.y = pack(y[1] * f, y[5] * f, 16.0f);
-                    w.z = pack(y[2] * f, y[6] * f, 1.0f);
-                    w.w = pack(y[3] * f, y[7] * f, 16.0f);
-                    qf[((r >> 3) * NW + j) * 32 + (r & 7) * 4 + tq] = w;
+                    // high and low byte (signed) of each, channels 0-7
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int n = __float2int_rn(x[8 * half + e] * f);
+                        hi[e] = static_cast<uint32_t>(n + 128) >> 8;
+                        lo[e] = static_cast<uint32_t>(n);
+                    }
+                    auto bytes = [](uint32_t p, uint32_t q, uint32_t u, uint32_t v) {
+                        return __byte_perm(__byte_perm(p, q, 0x0040), __byte_perm(u, v, 0x0040), 0x5410);
+                    };
+                    const uint2 high = make_uint2(bytes(hi[1], hi[3], hi[5], hi[7]), bytes(hi[0], hi[2], hi[4], hi[6]));
+                    const uint2 low = make_uint2(bytes(lo[1], lo[3], lo[5], lo[7]), bytes(lo[0], lo[2], lo[4], lo[6]));
+                    if constexpr (HALF) {
+                        qf[j * 32 + r * 4 + tq] = high;
+                        qf[j * 32 + (r + 4) * 4 + tq] = low;
+                    } else {
+                        qf[(((r >> 3) * NW + j) * 2) * 32 + (r & 7) * 4 + tq] = high;
+                        qf[(((r >> 3) * NW + j) * 2 + 1) * 32 + (r & 7) * 4 + tq] = low;
+                    }
                 }
             }
-            for (int k = 1; k < LANES; k <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
-            if (r < ROWS && part == 0) qoff[r] = -8.0f * frag::kCodeUnit * sum;
         }
         __syncthreads();
 
-        // thread's columns: queries 8 nt + 2 t4 and + 1
-        float cs[NT][2], off[NT][2];
+        // thread's columns of a tile: queries col0 and col0 + 1
+        float cs[NT][2];
         int cmax[NT][2];
         int least = 0x7FFFFFFF;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                cs[nt][x] = qs[8 * nt + 2 * t4 + x];
-                off[nt][x] = qoff[8 * nt + 2 * t4 + x];
-                cmax[nt][x] = qmax[8 * nt + 2 * t4 + x];
+                cs[nt][x] = qs[8 * nt + col0 + x];
+                cmax[nt][x] = qmax[8 * nt + col0 + x];
                 least = min(least, cmax[nt][x]);
             }
         for (int s = 1; s < 4; s <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, s));
         // the fragments stay in registers where there is room
-        uint4 qreg[NT == 1 ? NW : 1];
-        if constexpr (NT == 1)
+        uint2 qreg[HALF ? NW : 1];
+        if constexpr (HALF)
 #pragma unroll
             for (int j = 0; j < NW; ++j) qreg[j] = qf[j * 32 + lane];
 
@@ -593,17 +606,14 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 
         for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
             const int k0 = tile * TILE;
-            const uint32_t here = live[0];
+            const uint32_t here = live;
             // every query sees every key of the tile
             const bool all = here == (1u << NB) - 1 && k0 + TILE - 1 <= least;
-            if (!ptx::mbar_wait(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag)) break;
-            const uint8_t *st = ring + slot * STAGE;
-            const uint16_t *sks = reinterpret_cast<const uint16_t *>(st + TILE * D), *svs = sks + TILE;
-            float s[NB][NT][4];
+            if (!ptx::mbar_wait(key_bar, parity, &abort_flag)) break;
+            float s[NB][NT][NS];
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
-                const int ra = 16 * blk + sigma(g);
-                const uint8_t *pa = st + ra * (D / 2), *pb = pa + 8 * (D / 2);
+                const uint8_t *pa = st + (16 * blk + sigma(g)) * (D / 2), *pb = pa + 8 * (D / 2);
                 uint32_t ka[NW], kb[NW];
                 if constexpr (D == 64) {
                     *reinterpret_cast<uint2 *>(ka) = *reinterpret_cast<const uint2 *>(pa + 8 * t4);
@@ -615,45 +625,99 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                         reinterpret_cast<uint4 *>(kb)[i] = *reinterpret_cast<const uint4 *>(pb + 64 * i + 16 * t4);
                     }
                 }
+                int high[NT][4] = {}, low[HALF ? 1 : NT][4] = {};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int j = 0; j < NW; j += 2) {
+                    uint32_t ao[2], ae[2], bo[2], be[2];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) s[blk][nt][x] = off[nt][x & 1];
+                    for (int y = 0; y < 2; ++y) {
+                        frag::codes_s8(ka[j + y], ao[y], ae[y]);
+                        frag::codes_s8(kb[j + y], bo[y], be[y]);
+                    }
+                    if constexpr (HALF) {
+                        frag::mma_s8(high[0], ao[0], bo[0], ao[1], bo[1], qreg[j].x, qreg[j + 1].x);
+                        frag::mma_s8(high[0], ae[0], be[0], ae[1], be[1], qreg[j].y, qreg[j + 1].y);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < NW; ++j) {
-                    uint32_t wa[4], wb[4];
-                    frag::codes_f16(masks, ka[j], wa);
-                    frag::codes_f16(masks, kb[j], wb);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 q = NT == 1 ? qreg[j] : qf[(nt * NW + j) * 32 + lane];
-                        frag::mma_f16(s[blk][nt], wa[0], wb[0], wa[1], wb[1], q.x, q.y);
-                        frag::mma_f16(s[blk][nt], wa[2], wb[2], wa[3], wb[3], q.z, q.w);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 *q = qf + (nt * NW + j) * 64 + lane;
+                            const uint2 h0 = q[0], l0 = q[32], h1 = q[64], l1 = q[96];
+                            frag::mma_s8(high[nt], ao[0], bo[0], ao[1], bo[1], h0.x, h1.x);
+                            frag::mma_s8(low[nt], ao[0], bo[0], ao[1], bo[1], l0.x, l1.x);
+                            frag::mma_s8(high[nt], ae[0], be[0], ae[1], be[1], h0.y, h1.y);
+                            frag::mma_s8(low[nt], ae[0], be[0], ae[1], be[1], l0.y, l1.y);
+                        }
                     }
                 }
-                // scores in units of log2
-                const float ska = frag::bf16_f32(sks[ra]), skb = frag::bf16_f32(sks[ra + 8]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                // 256 high + low, exact in 32 bits, and the scores in units of log2
+                const float ska = frag::bf16_f32(sks[16 * blk + key0]);
+                if constexpr (HALF) {
+                    // columns 0-3 have the high bytes' sums and columns 4-7 the
+                    // low ones': lanes of columns 0-3 take rows 0-7, the others
+                    // rows 8-15
+                    const bool first = t4 < 2;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        s[blk][nt][x] *= ska * cs[nt][x];
-                        s[blk][nt][2 + x] *= skb * cs[nt][x];
+                        const int mine = first ? high[0][x] : high[0][2 + x];
+                        const int theirs = __shfl_xor_sync(0xFFFFFFFFu, first ? high[0][2 + x] : high[0][x], 2);
+                        const int sum = 256 * (first ? mine : theirs) + (first ? theirs : mine);
+                        s[blk][0][x] = static_cast<float>(sum) * (ska * cs[0][x]);
                     }
-            }
-            if (!all) {
-                // hidden keys are -inf whatever they hold
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk) {
-                    const int ja = k0 + 16 * blk + sigma(g);
-                    const bool there = (here >> blk) & 1;
+                } else {
+                    const float skb = frag::bf16_f32(sks[16 * blk + key0 + 8]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
+                            s[blk][nt][x] = static_cast<float>(256 * high[nt][x] + low[nt][x]) * ((x < 2 ? ska : skb) * cs[nt][x & 1]);
+                }
+            }
+            __syncwarp();               // the keys have been read
+            const bool more = tile + kAttnWarps < tile1;
+            if (more) request(tile + kAttnWarps);
+            if (!all) {
+                // hidden keys are -inf whatever they hold
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk) {
+                    const int ja = k0 + 16 * blk + key0;
+                    const bool there = (here >> blk) & 1;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < NS; ++x)
                             if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) s[blk][nt][x] = -INFINITY;
                 }
             }
+            // ---- running maximum and sum
+            float mul[NT][2];
+            bool turn = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float top = m[nt][x];
+#pragma unroll
+                    for (int blk = 0; blk < NB; ++blk) {
+                        if constexpr (HALF) top = fmaxf(top, s[blk][nt][x]);
+                        else top = prep::max3(top, s[blk][nt][x], s[blk][nt][2 + x]);
+                    }
+                    for (int k = HALF ? 2 : 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+                    const float safe = top == -INFINITY ? 0.0f : top;
+                    mul[nt][x] = ex2(m[nt][x] - safe);
+                    turn |= top != m[nt][x];
+                    m[nt][x] = top;
+                    l[nt][x] *= mul[nt][x];
+#pragma unroll
+                    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                        for (int y = 0; y < NS; y += 2) {
+                            const float p = ex2(s[blk][nt][y + x] - safe);
+                            l[nt][x] += p;
+                            s[blk][nt][y + x] = p;
+                        }
+                }
+            if (!ptx::mbar_wait(value_bar, parity, &abort_flag)) break;
+            parity ^= 1;
             // the largest exponent of the values' scales so far; hidden and
             // infinite ones do not count
             uint32_t top_bits = 0;
@@ -666,58 +730,36 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             }
             const uint32_t exponent = __reduce_max_sync(0xFFFFFFFFu, top_bits) >> 7;
             float shift = 1.0f;
-            bool turn = exponent > ref;
-            if (turn) {
+            if (exponent > ref) {
+                turn = true;
                 shift = exponent - ref < 127 ? __uint_as_float((127 - (exponent - ref)) << 23) : 0.0f;
                 ref = exponent;
             }
             const float unit = __uint_as_float((127 + 14 + 127 - ref) << 23);   // 2^14 over the reference
-            // ---- running maximum and sum
-            float mul[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float top = m[nt][x];
-#pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) top = prep::max3(top, s[blk][nt][x], s[blk][nt][2 + x]);
-                    for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-                    const float safe = top == -INFINITY ? 0.0f : top;
-                    mul[nt][x] = ex2(m[nt][x] - safe);
-                    turn |= top != m[nt][x];
-                    m[nt][x] = top;
-                    l[nt][x] *= mul[nt][x];
-#pragma unroll
-                    for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-                        for (int y = 0; y < 4; y += 2) {
-                            const float p = ex2(s[blk][nt][y + x] - safe);
-                            l[nt][x] += p;
-                            s[blk][nt][y + x] = p;
-                        }
-                    mul[nt][x] *= shift;
-                }
             // ---- weights of the values, as f16 fragments, and their sums
             uint32_t p0[NB][NT], p1[NB][NT];
             float psum[NT][4] = {};
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
-                const float sva = unit * frag::bf16_f32(svs[16 * blk + sigma(g)]);
-                const float svb = unit * frag::bf16_f32(svs[16 * blk + sigma(g) + 8]);
+                const float sva = unit * frag::bf16_f32(svs[16 * blk + key0]);
+                const float svb = HALF ? 0.0f : unit * frag::bf16_f32(svs[16 * blk + key0 + 8]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
+                    float w[NS];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = s[blk][nt][x] * (x < 2 ? sva : svb);
+                    for (int x = 0; x < NS; ++x) w[x] = s[blk][nt][x] * (x < 2 ? sva : svb);
                     if (!all) {         // a hidden key's scale may be anything
-                        const int ja = k0 + 16 * blk + sigma(g);
+                        const int ja = k0 + 16 * blk + key0;
                         const bool there = (here >> blk) & 1;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
+                        for (int x = 0; x < NS; ++x)
                             if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) w[x] = 0.0f;
                     }
                     p0[blk][nt] = frag::transpose8x8(frag::pack_f16(w[0], w[1]));
-                    p1[blk][nt] = frag::transpose8x8(frag::pack_f16(w[2], w[3]));
+                    // HALF: rows 4-7 of the transpose are the keys 8-15 of
+                    // queries 0-3; columns 4-7 of the product are not used
+                    if constexpr (HALF) p1[blk][nt] = __shfl_xor_sync(0xFFFFFFFFu, p0[blk][nt], 16);
+                    else p1[blk][nt] = frag::transpose8x8(frag::pack_f16(w[2], w[3]));
                     frag::mma_f16(psum[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p0[blk][nt], p1[blk][nt]);
                 }
             }
@@ -727,7 +769,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= mul[nt][x & 1];
+                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= shift * mul[nt][x & 1];
             }
             // the codes' offset of 8, taken off tile by tile so that it never
             // grows far beyond the sums it is part of
@@ -768,27 +810,20 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                             frag::mma_f16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p0[blk][nt], p1[blk][nt]);
                 }
             }
-            __syncwarp();               // the slot has been read
-#pragma unroll
-            for (int i = 0; i + 1 < DEPTH; ++i) live[i] = live[i + 1];
-            const int far = tile + DEPTH * kAttnWarps;
-            if (far < tile1) live[DEPTH - 1] = request(far, slot);
-            if (++slot == DEPTH) {
-                slot = 0;
-                parity ^= 1;
-            }
+            __syncwarp();               // the values have been read
+            if (more) copy(1);
         }
 
         // ---- join the warps
-        __syncthreads();                // every ring is drained
+        __syncthreads();                // every tile is done
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                for (int k = 4; k < 32; k <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], k);
+                for (int k = HALF ? 2 : 4; k < 32; k <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], k);
                 if (g == 0) {
-                    wm[warp][8 * nt + 2 * t4 + x] = m[nt][x];
-                    wl[warp][8 * nt + 2 * t4 + x] = l[nt][x];
+                    wm[warp][8 * nt + col0 + x] = m[nt][x];
+                    wl[warp][8 * nt + col0 + x] = l[nt][x];
                 }
             }
         if (lane == 0) wunit[warp] = __uint_as_float((ref - 14) << 23);
@@ -798,7 +833,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    osum[(warp * ROWS + 8 * nt + 2 * t4 + (x & 1)) * PITCH + (D / 8) * g + 8 * (i >> 2) + (i & 3) +
+                    if (!HALF || t4 < 2) osum[(warp * ROWS + 8 * nt + 2 * t4 + (x & 1)) * PITCH + (D / 8) * g + 8 * (i >> 2) + (i & 3) +
                          4 * (x >> 1)] = o[i][nt][x] * ((i & 1) ? 1.0f / (16.0f * frag::kCodeUnit) : 1.0f / frag::kCodeUnit);
         __syncthreads();
         const bool whole = seg_u0 >= u0 && seg_u1 <= u1;
@@ -837,7 +872,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
                 for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
         }
-        ptx::fence_proxy_async_smem();  // these reads and writes come before the next copies into the rings
+        ptx::fence_proxy_async_smem();  // these reads and writes come before the next copies into the stages
         if (!whole && seg_u0 >= u0 && tid == 0)
             a.desc[blockIdx.x] = make_int4(static_cast<int>((seg_u1 - 1) / share), b, h, rb);
         u = seg_u0 + tile1;
@@ -846,13 +881,13 @@ __global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttnArgs a) {
 
 // CTA c joins the parts of the request that CTA c of attention_kernel began
 // and did not end.
-template <int D, int NT>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
-    constexpr int ROWS = 8 * NT, LANES = D / 16;
+    constexpr int LANES = D / 16;
     ptx::grid_dependency_wait();
     const int4 d = a.desc[blockIdx.x];
     if (d.x < 0) return;
-    const Request rq = request_of<D, ROWS>(a, d.y);
+    const Request rq = request_of<ROWS>(a, d.y);
     for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
         const int i = i0 + static_cast<int>(threadIdx.x);
         const int r = min(i / LANES, ROWS - 1), part = i % LANES;
@@ -879,9 +914,10 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
     }
 }
 
-template <int D, int NT>
+template <int D, int ROWS>
 constexpr int attn_smem() {
-    return NT * (D / 32) * 512 + kAttnWarps * ring_depth(D) * tile_keys(D) * (D + 4);
+    constexpr int stages = kTile * (D + 4), outputs = ROWS * (D + 4) * 4;
+    return (ROWS / 4) * (D / 32) * 256 + kAttnWarps * (stages > outputs ? stages : outputs);
 }
 
 }  // namespace kv4
@@ -900,14 +936,17 @@ bool set_smem(F *kernel, int bytes) {
 convrot_status setup(int *dev) {
     return host::device_setup(dev, [] {
         bool ok = set_smem(plan_kernel, 3 * (CONVROT_KV4_MAX_REQUESTS + 1) * 4);
-        ok &= set_smem(attention_kernel<64, 1>, attn_smem<64, 1>());
-        ok &= set_smem(attention_kernel<64, 2>, attn_smem<64, 2>());
         ok &= set_smem(attention_kernel<64, 4>, attn_smem<64, 4>());
-        ok &= set_smem(attention_kernel<128, 1>, attn_smem<128, 1>());
-        ok &= set_smem(attention_kernel<128, 2>, attn_smem<128, 2>());
+        ok &= set_smem(attention_kernel<64, 8>, attn_smem<64, 8>());
+        ok &= set_smem(attention_kernel<64, 16>, attn_smem<64, 16>());
+        ok &= set_smem(attention_kernel<64, 32>, attn_smem<64, 32>());
         ok &= set_smem(attention_kernel<128, 4>, attn_smem<128, 4>());
-        ok &= set_smem(attention_kernel<256, 1>, attn_smem<256, 1>());
-        ok &= set_smem(attention_kernel<256, 2>, attn_smem<256, 2>());
+        ok &= set_smem(attention_kernel<128, 8>, attn_smem<128, 8>());
+        ok &= set_smem(attention_kernel<128, 16>, attn_smem<128, 16>());
+        ok &= set_smem(attention_kernel<128, 32>, attn_smem<128, 32>());
+        ok &= set_smem(attention_kernel<256, 4>, attn_smem<256, 4>());
+        ok &= set_smem(attention_kernel<256, 8>, attn_smem<256, 8>());
+        ok &= set_smem(attention_kernel<256, 16>, attn_smem<256, 16>());
         return ok;
     });
 }
@@ -952,17 +991,17 @@ unsigned row_grid(int64_t threads, int sms) {
     return static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
 }
 
-// Query columns of the product: the smallest of 8, 16 and 32 (16 with D = 256,
-// whose accumulators fill the registers) that holds an average request's rows.
-int row_tiles(int64_t T, int64_t B, int G, int D) {
+// Rows of a block: the smallest of 4, 8, 16 and 32 (16 with D = 256, whose
+// accumulators fill the registers) that holds an average request's rows.
+int block_rows(int64_t T, int64_t B, int G, int D) {
     const int64_t rows = (T + B - 1) / B * G;
-    return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
+    return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
 }
 
 // CTAs that can have work at most, from what the host knows.
-int64_t attn_ctas(int64_t T, int64_t B, int G, int kv_heads, int NT, int D, int64_t max_keys) {
-    const int64_t blocks = (T * G + 8 * NT - 1) / (8 * NT) + B;
-    const int64_t tiles = (max_keys + tile_keys(D) - 1) / tile_keys(D);
+int64_t attn_ctas(int64_t T, int64_t B, int G, int kv_heads, int rows, int64_t max_keys) {
+    const int64_t blocks = (T * G + rows - 1) / rows + B;
+    const int64_t tiles = (max_keys + kTile - 1) / kTile;
     // beyond kMaxCtas the product is not needed, and could overflow
     if (blocks > 8 * kMaxCtas || tiles > 8 * kMaxCtas) return kMaxCtas;
     const int64_t n = (blocks * (tiles > 0 ? tiles : 1) * kv_heads + kMinUnits - 1) / kMinUnits;
@@ -975,16 +1014,16 @@ bool attn_shape_ok(int64_t T, int64_t B, int heads, int kv_heads, int D, int64_t
            (D == 64 || D == 128 || D == 256) && max_keys >= 0 && max_keys < (int64_t(1) << 31);
 }
 
-template <int D, int NT>
+template <int D, int ROWS>
 convrot_status launch_attention(AttnArgs a, int64_t ctas, int sms, cudaStream_t stream) {
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_kernel<D, NT>, kAttnThreads,
-                                                      attn_smem<D, NT>()) != cudaSuccess)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_kernel<D, ROWS>, kAttnThreads,
+                                                      attn_smem<D, ROWS>()) != cudaSuccess)
         return CONVROT_ERR_CUDA;
     if (ctas > static_cast<int64_t>(sms) * per_sm) ctas = static_cast<int64_t>(sms) * per_sm;
-    attention_kernel<D, NT><<<static_cast<unsigned>(ctas), kAttnThreads, attn_smem<D, NT>(), stream>>>(a);
+    attention_kernel<D, ROWS><<<static_cast<unsigned>(ctas), kAttnThreads, attn_smem<D, ROWS>(), stream>>>(a);
     if (launched() != CONVROT_OK) return CONVROT_ERR_CUDA;
-    return host::launch_dependent(combine_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), dim3(kAttnThreads), 0,
+    return host::launch_dependent(combine_kernel<D, ROWS>, dim3(static_cast<unsigned>(ctas)), dim3(kAttnThreads), 0,
                                   stream, a);
 }
 
@@ -1068,9 +1107,9 @@ convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *s
 size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int kv_heads,
                                             int head_dim, int64_t max_keys) {
     if (!attn_shape_ok(T, B, heads, kv_heads, head_dim, max_keys) || T == 0 || B == 0) return 0;
-    const int G = heads / kv_heads, NT = row_tiles(T, B, G, head_dim);
-    const size_t ctas = static_cast<size_t>(attn_ctas(T, B, G, kv_heads, NT, head_dim, max_keys));
-    return host::round256(ctas * sizeof(int4)) + ctas * 2 * 8 * NT * (head_dim + 2) * sizeof(float);
+    const int G = heads / kv_heads, rows = block_rows(T, B, G, head_dim);
+    const size_t ctas = static_cast<size_t>(attn_ctas(T, B, G, kv_heads, rows, max_keys));
+    return host::round256(ctas * sizeof(int4)) + ctas * 2 * rows * (head_dim + 2) * sizeof(float);
 }
 
 convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void *q_bf16,
@@ -1097,20 +1136,24 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
     if ((st = host::check_device_ptrs(dev, {q_bf16, block_table, seq_lens, cu_q, out_bf16, workspace, cache->k_codes,
                                             cache->k_scales, cache->v_codes, cache->v_scales})) != CONVROT_OK)
         return st;
-    const int G = heads / cache->kv_heads, NT = row_tiles(T, B, G, D);
-    const int64_t ctas = attn_ctas(T, B, G, cache->kv_heads, NT, D, max_pages * cache->page);
+    const int G = heads / cache->kv_heads, rows = block_rows(T, B, G, D);
+    const int64_t ctas = attn_ctas(T, B, G, cache->kv_heads, rows, max_pages * cache->page);
     AttnArgs a{device_cache(cache), static_cast<const uint16_t *>(q_bf16), ldq, T, G, block_table, max_pages,
                seq_lens, cu_q, static_cast<int>(B), scale * 1.4426950408889634f, static_cast<int4 *>(workspace),
                reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(ctas * sizeof(int4))),
                static_cast<uint16_t *>(out_bf16)};
     const int sms = host::g_dev[dev].num_sms;
-    if (D == 64)
-        return NT == 1 ? launch_attention<64, 1>(a, ctas, sms, stream)
-                       : NT == 2 ? launch_attention<64, 2>(a, ctas, sms, stream) : launch_attention<64, 4>(a, ctas, sms, stream);
-    if (D == 128)
-        return NT == 1 ? launch_attention<128, 1>(a, ctas, sms, stream)
-                       : NT == 2 ? launch_attention<128, 2>(a, ctas, sms, stream) : launch_attention<128, 4>(a, ctas, sms, stream);
-    return NT == 1 ? launch_attention<256, 1>(a, ctas, sms, stream) : launch_attention<256, 2>(a, ctas, sms, stream);
+    auto go = [&](auto d) {
+        constexpr int DIM = decltype(d)::value;
+        switch (rows) {
+            case 4: return launch_attention<DIM, 4>(a, ctas, sms, stream);
+            case 8: return launch_attention<DIM, 8>(a, ctas, sms, stream);
+            case 16: return launch_attention<DIM, 16>(a, ctas, sms, stream);
+        }
+        return launch_attention<DIM, DIM == 256 ? 16 : 32>(a, ctas, sms, stream);
+    };
+    return D == 64 ? go(std::integral_constant<int, 64>{})
+                   : D == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 256>{});
 }
 
 convrot_status convrot_kv4_check_device_error(convrot_stream_t stream) {

@@ -97,12 +97,10 @@ def attention(q, cache, table, lens, cu_q, scale, group, dead=()):
                     s = kk @ qr * scale
                     p = torch.softmax(s, 0)
                     out[a + i, hq] = rotate(p @ vv, group)
-                    # scores: f16 queries (2^-11 of each value, 2^-34 of the
-                    # row's largest), fp32 rotation and sums (2^-17 of the terms,
-                    # and of 8 s_k sum |q|, the offset that the codes carry:
-                    # up to 16 steps, each off by at most an ulp, 2^-23)
-                    l1 = kk.abs() @ (qr.abs() * (2.0 ** -11 + 2.0 ** -17) + qr.abs().max() * (2.0 ** -34 + 1e-5)) * abs(scale)
-                    l1 = l1 + ks_rows(ks, row, n, h)[seen] * (8 * qr.abs().sum() * 16 * 2.0 ** -23 * abs(scale))
+                    # scores: 16-bit queries (half a step of the row's largest
+                    # / 32000: 2^-16 of it), fp32 rotation (1e-5 of it), exact
+                    # sums, three fp32 products (2^-17 of the terms)
+                    l1 = kk.abs() @ (qr.abs() * 2.0 ** -17 + qr.abs().max() * (2.0 ** -16 + 1e-5)) * abs(scale)
                     # and the maximum taken off in fp32 (2^-24 of the score), exp2f 2 ulp
                     ds = float((l1 + s.abs() * 2.0 ** -22).max()) + 2.0 ** -22
                     # weights: both the numerator and the sum move by ds; P s_v in

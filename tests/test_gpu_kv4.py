@@ -10,10 +10,9 @@ Gates:
     back keeps 2-norms, the output's rounding is off by 2^-8 of each value, and
       e = expm1(2 ds) + 2^-11 + 2^-16:
     each weight p_j is off by at most the factor exp(2 ds) for scores off by
-    ds (decoding_ref.attention adds ds up: f16 queries, fp32 rotation and sums,
-    exp2), its product with the value's scale is rounded to f16 (2^-11), and
+    ds (decoding_ref.attention adds ds up: 16-bit queries, fp32 rotation, exp2), its product with the value's scale is rounded to f16 (2^-11), and
     the fp32 sums and joins of parts stay below 2^-16; two small terms for the
-    offset that the codes carry and for weights below the f16 range.
+    offset that the values' codes carry and for weights below the f16 range.
 """
 import pytest
 import torch
