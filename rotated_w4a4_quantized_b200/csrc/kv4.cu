@@ -283,7 +283,8 @@ read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *_
 //   columns; the sums are exact in int32.  Up to 4 rows fill the 8 columns of
 //   one product with both bytes, and each lane then has two scores of a block
 //   instead of four.
-// - V: f16 subnormals offset by 8 (frag::codes_f16); the offset's part of the
+// - V: f16 subnormals offset by 8 (frag::codes_f16), five operations for 8
+//   codes with up to 4 rows, else six; the offset's part of the
 //   outputs, -8 times the sum of the weights, comes out of one more product
 //   with a matrix of ones and is taken off before each tile.
 // P s_v is f16 relative to the largest exponent of s_v so far (powers of two;
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     constexpr int NS = HALF ? 2 : 4;    // scores a thread, 16-key block and column tile
     constexpr int NW = D / 32;          // K words (8 codes) a thread and key
     constexpr int VW = D / 64;          // V words a thread and key
-    constexpr int MT = D / 16;          // 16-row blocks of O^T
+    constexpr int MT = HALF ? D / 32 : D / 16;   // accumulators of O^T, four values each
     constexpr int LANES = D / 16;
     constexpr int PITCH = D + 4;
     constexpr int TILE = kTile, NB = TILE / 16;
@@ -407,6 +408,9 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     __shared__ long long scan[kAttnWarps];
     __shared__ long long start_unit;
     __shared__ int start_b;
+
+    // whether value x of accumulator i belongs to the second nibble of a byte
+    auto second_nibble = [](int i, int x) { return HALF && VW == 1 ? (x >> 1) != 0 : (i & 1) != 0; };
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -467,7 +471,16 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     // this thread's row in a 16-key block, of its first scores
     const int key0 = sigma(g) + (HALF && t4 >= 2 ? 8 : 0);
     const int col0 = HALF ? 2 * (t4 & 1) : 2 * t4;   // and its first query of a column tile
-    const int piece_shift = min(a.c.page_shift, 6);   // keys of a tile in one page
+    const bool first = t4 < 2;
+    const int weight_mine = first ? 256 : 1, weight_theirs = first ? 1 : 256;
+    // HALF: the transposed weights of two keys -> (low, 0) and (high, 0) for
+    // columns 0-3, (0, low) and (0, high) for columns 4-7
+    const uint32_t pick_low = g < 4 ? 0x4410u : 0x1044u, pick_high = g < 4 ? 0x4432u : 0x3244u;
+    // keys of a tile in one page, the average bytes of a lane's copy, and the
+    // lanes that copy a whole tile
+    const int piece_shift = min(a.c.page_shift, 6), run_half = (D / 2 + 2) << (piece_shift - 1);
+    const uint32_t every_run = TILE >> piece_shift == 1 ? 3u : TILE >> piece_shift == 2 ? 15u : 255u;
+    const int page_mask = (1 << a.c.page_shift) - 1, num_pages = static_cast<int>(a.c.num_pages);   // keys of a tile in one page
 
     for (long long u = u0; u < u1;) {
         Request rq = request_of<ROWS>(a, b);
@@ -490,33 +503,29 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
         // Request a tile's keys; its values are requested once the last
         // tile's have been read.  Lane 2 p + i copies the codes (i = 0) or the
         // scales of the p-th run of keys that lie in one page.
-        int64_t run_row = -1;           // the run's first row in the cache
-        uint32_t live = 0, runs = 0;    // 16-key blocks that are there; lanes that copy
-        const int run = (lane >> 1) << piece_shift, run_keys = 1 << piece_shift;
+        const int run = (lane >> 1) << piece_shift;
+        const int unit_bytes = (lane & 1) ? 2 : D / 2;              // of a key
+        const int64_t head_at = (static_cast<int64_t>(h) << a.c.page_shift) * unit_bytes;
+        const uint8_t *key_base = ((lane & 1) ? reinterpret_cast<const uint8_t *>(a.c.ks) : a.c.kc) + head_at;
+        const uint8_t *value_base = ((lane & 1) ? reinterpret_cast<const uint8_t *>(a.c.vs) : a.c.vc) + head_at;
+        const int page_bytes = (a.c.heads << a.c.page_shift) * unit_bytes;
+        int64_t run_at = -1;            // the run's place behind the base, -1: none
+        uint32_t runs = 0;              // lanes that copy
         auto copy = [&](int i) {        // keys (0) or values (1)
             const uint32_t bar = i ? value_bar : key_bar;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (__popc(runs) >> 1) * (run_keys * (D / 2 + 2)));
-            if (run_row >= 0) {
-                if (lane & 1)
-                    bulk_load(st_s + TILE * D + i * (TILE * 2) + run * 2, (i ? a.c.vs : a.c.ks) + run_row, run_keys * 2, bar);
-                else
-                    bulk_load(st_s + i * (TILE * D / 2) + run * (D / 2), (i ? a.c.vc : a.c.kc) + run_row * (D / 2),
-                              run_keys * (D / 2), bar);
-            }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, __popc(runs) * run_half);
+            if (run_at >= 0)
+                bulk_load(((lane & 1) ? st_s + TILE * D + i * (TILE * 2) : st_s + i * (TILE * D / 2)) + run * unit_bytes,
+                          (i ? value_base : key_base) + run_at, unit_bytes << piece_shift, bar);
         };
         auto request = [&](int tile) {
             const int j0 = tile * TILE + run;
             const bool want = run < TILE && j0 < rq.len;
             const int id = want ? table[j0 >> a.c.page_shift] : -1;
-            const bool there = want && id >= 0 && id < a.c.num_pages;
+            const bool there = id >= 0 && id < num_pages;
             if (want && !there) page_error();
-            run_row = there ? ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) +
-                                  (j0 & ((1 << a.c.page_shift) - 1))
-                            : -1;
+            run_at = there ? static_cast<int64_t>(id) * page_bytes + (j0 & page_mask) * unit_bytes : -1;
             runs = __ballot_sync(0xFFFFFFFFu, there);
-            live = 0;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) live |= ((runs >> (2 * ((16 * i) >> piece_shift))) & 1u) << i;
             copy(0);
         };
         if (tile0 + warp < tile1) {
@@ -606,9 +615,9 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 
         for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
             const int k0 = tile * TILE;
-            const uint32_t here = live;
+            const uint32_t here = runs;
             // every query sees every key of the tile
-            const bool all = here == (1u << NB) - 1 && k0 + TILE - 1 <= least;
+            const bool all = here == every_run && k0 + TILE - 1 <= least;
             if (!ptx::mbar_wait(key_bar, parity, &abort_flag)) break;
             float s[NB][NT][NS];
 #pragma unroll
@@ -655,12 +664,11 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                     // columns 0-3 have the high bytes' sums and columns 4-7 the
                     // low ones': lanes of columns 0-3 take rows 0-7, the others
                     // rows 8-15
-                    const bool first = t4 < 2;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int mine = first ? high[0][x] : high[0][2 + x];
                         const int theirs = __shfl_xor_sync(0xFFFFFFFFu, first ? high[0][2 + x] : high[0][x], 2);
-                        const int sum = 256 * (first ? mine : theirs) + (first ? theirs : mine);
+                        const int sum = mine * weight_mine + theirs * weight_theirs;
                         s[blk][0][x] = static_cast<float>(sum) * (ska * cs[0][x]);
                     }
                 } else {
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 #pragma unroll
                 for (int blk = 0; blk < NB; ++blk) {
                     const int ja = k0 + 16 * blk + key0;
-                    const bool there = (here >> blk) & 1;
+                    const bool there = (here >> (2 * ((16 * blk) >> piece_shift))) & 1;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -721,14 +729,17 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
             // the largest exponent of the values' scales so far; hidden and
             // infinite ones do not count
             uint32_t top_bits = 0;
-            if (2 * lane < TILE) {
+            {
                 const uint32_t two = reinterpret_cast<const uint32_t *>(svs)[lane];
-                const bool there = (here >> (lane >> 3)) & 1;
-                const uint32_t lo = two & 0xFFFFu, hi = two >> 16;
-                if (there && k0 + 2 * lane < rq.len && lo < 0x7F80u) top_bits = lo;
-                if (there && k0 + 2 * lane + 1 < rq.len && hi < 0x7F80u) top_bits = max(top_bits, hi);
+                uint32_t lo = two & 0xFFFFu, hi = two >> 16;
+                if (!all) {
+                    const bool there = (here >> (2 * ((2 * lane) >> piece_shift))) & 1;
+                    if (!there || k0 + 2 * lane >= rq.len || lo >= 0x7F80u) lo = 0;
+                    if (!there || k0 + 2 * lane + 1 >= rq.len || hi >= 0x7F80u) hi = 0;
+                }
+                top_bits = max(lo, hi);
             }
-            const uint32_t exponent = __reduce_max_sync(0xFFFFFFFFu, top_bits) >> 7;
+            const uint32_t exponent = min(__reduce_max_sync(0xFFFFFFFFu, top_bits) >> 7, 254u);
             float shift = 1.0f;
             if (exponent > ref) {
                 turn = true;
@@ -737,7 +748,8 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
             }
             const float unit = __uint_as_float((127 + 14 + 127 - ref) << 23);   // 2^14 over the reference
             // ---- weights of the values, as f16 fragments, and their sums
-            uint32_t p0[NB][NT], p1[NB][NT];
+            // HALF: p[blk][0][..] are the keys of rows 0-7 (two of them) and rows 8-15
+            uint32_t p[NB][NT][HALF ? 4 : 2];
             float psum[NT][4] = {};
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
@@ -750,17 +762,28 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                     for (int x = 0; x < NS; ++x) w[x] = s[blk][nt][x] * (x < 2 ? sva : svb);
                     if (!all) {         // a hidden key's scale may be anything
                         const int ja = k0 + 16 * blk + key0;
-                        const bool there = (here >> blk) & 1;
+                        const bool there = (here >> (2 * ((16 * blk) >> piece_shift))) & 1;
 #pragma unroll
                         for (int x = 0; x < NS; ++x)
                             if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) w[x] = 0.0f;
                     }
-                    p0[blk][nt] = frag::transpose8x8(frag::pack_f16(w[0], w[1]));
-                    // HALF: rows 4-7 of the transpose are the keys 8-15 of
-                    // queries 0-3; columns 4-7 of the product are not used
-                    if constexpr (HALF) p1[blk][nt] = __shfl_xor_sync(0xFFFFFFFFu, p0[blk][nt], 16);
-                    else p1[blk][nt] = frag::transpose8x8(frag::pack_f16(w[2], w[3]));
-                    frag::mma_f16(psum[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p0[blk][nt], p1[blk][nt]);
+                    const uint32_t mine = frag::transpose8x8(frag::pack_f16(w[0], w[1]));
+                    if constexpr (HALF) {
+                        // lanes of columns 0-3 hold rows 0-7 of a query, those
+                        // of columns 4-7 rows 8-15
+                        const uint32_t theirs = __shfl_xor_sync(0xFFFFFFFFu, mine, 16);
+                        const uint32_t upper = g < 4 ? mine : theirs, lower = g < 4 ? theirs : mine;
+                        p[blk][nt][0] = __byte_perm(upper, 0, pick_low);
+                        p[blk][nt][1] = __byte_perm(upper, 0, pick_high);
+                        p[blk][nt][2] = __byte_perm(lower, 0, pick_low);
+                        p[blk][nt][3] = __byte_perm(lower, 0, pick_high);
+                    } else {
+                        p[blk][nt][0] = mine;
+                        p[blk][nt][1] = frag::transpose8x8(frag::pack_f16(w[2], w[3]));
+                    }
+#pragma unroll
+                    for (int y = 0; y < (HALF ? 4 : 2); y += 2)
+                        frag::mma_f16(psum[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[blk][nt][y], p[blk][nt][y + 1]);
                 }
             }
             if (__any_sync(0xFFFFFFFFu, turn)) {
@@ -780,7 +803,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) o[i][nt][x] += (i & 1) ? second[x & 1] : one[x & 1];
+                    for (int x = 0; x < 4; ++x) o[i][nt][x] += second_nibble(i, x) ? second[x & 1] : one[x & 1];
             }
             // ---- O^T += V^T P^T
 #pragma unroll
@@ -795,19 +818,46 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                     else if constexpr (VW == 2) *reinterpret_cast<uint2 *>(v[i]) = *reinterpret_cast<const uint2 *>(p);
                     else *reinterpret_cast<uint4 *>(v[i]) = *reinterpret_cast<const uint4 *>(p);
                 }
+                if constexpr (HALF) {
+                    // A register has codes i and i + 4 of one key's word: two
+                    // rows of O^T that the columns tell apart, so that no
+                    // keys have to be put side by side.  Rows r and r + 8 of a
+                    // product are neighbouring words (with D = 64, which has
+                    // one word a lane, its even and odd pairs).
 #pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    // halves of two keys side by side: codes 0-3, then 4-7
-                    uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
-                    frag::codes_f16(masks, __byte_perm(v[0][w], v[1][w], 0x5410), lo0);
-                    frag::codes_f16(masks, __byte_perm(v[0][w], v[1][w], 0x7632), hi0);
-                    frag::codes_f16(masks, __byte_perm(v[2][w], v[3][w], 0x5410), lo1);
-                    frag::codes_f16(masks, __byte_perm(v[2][w], v[3][w], 0x7632), hi1);
+                    for (int y = 0; y < 4; y += 2)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                        for (int w = 0; w < VW; w += 2) {
+                            uint32_t a0[4], a1[4], a2[4], a3[4];
+                            frag::codes_f16(masks, v[y][w], a0);
+                            frag::codes_f16(masks, v[y + 1][w], a2);
+                            if constexpr (VW > 1) {
+                                frag::codes_f16(masks, v[y][w + 1], a1);
+                                frag::codes_f16(masks, v[y + 1][w + 1], a3);
+                            }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            frag::mma_f16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p0[blk][nt], p1[blk][nt]);
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (VW > 1)
+                                    frag::mma_f16(o[2 * w + i][0], a0[i], a1[i], a2[i], a3[i], p[blk][0][y], p[blk][0][y + 1]);
+                                else if (i < 2)
+                                    frag::mma_f16(o[i][0], a0[2 * i], a0[2 * i + 1], a2[2 * i], a2[2 * i + 1], p[blk][0][y], p[blk][0][y + 1]);
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        // halves of two keys side by side: codes 0-3, then 4-7
+                        uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
+                        frag::codes_f16(masks, __byte_perm(v[0][w], v[1][w], 0x5410), lo0);
+                        frag::codes_f16(masks, __byte_perm(v[0][w], v[1][w], 0x7632), hi0);
+                        frag::codes_f16(masks, __byte_perm(v[2][w], v[3][w], 0x5410), lo1);
+                        frag::codes_f16(masks, __byte_perm(v[2][w], v[3][w], 0x7632), hi1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                frag::mma_f16(o[4 * w + i][nt], lo0[i], hi0[i], lo1[i], hi1[i], p[blk][nt][0], p[blk][nt][1]);
+                    }
                 }
             }
             __syncwarp();               // the values have been read
@@ -832,9 +882,12 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (!HALF || t4 < 2) osum[(warp * ROWS + 8 * nt + 2 * t4 + (x & 1)) * PITCH + (D / 8) * g + 8 * (i >> 2) + (i & 3) +
-                         4 * (x >> 1)] = o[i][nt][x] * ((i & 1) ? 1.0f / (16.0f * frag::kCodeUnit) : 1.0f / frag::kCodeUnit);
+                for (int x = 0; x < 4; ++x) {
+                    const int d = (D / 8) * g + (HALF ? (first ? 0 : 4) + (VW > 1 ? 8 * (2 * (i >> 2) + (x >> 1)) + (i & 3) : 2 * i + (x >> 1))
+                                                      : 8 * (i >> 2) + (i & 3) + 4 * (x >> 1));
+                    osum[(warp * ROWS + 8 * nt + col0 + (x & 1)) * PITCH + d] =
+                        o[i][nt][x] * (second_nibble(i, x) ? 1.0f / (16.0f * frag::kCodeUnit) : 1.0f / frag::kCodeUnit);
+                }
         __syncthreads();
         const bool whole = seg_u0 >= u0 && seg_u1 <= u1;
         float *part_out = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (seg_u0 >= u0 ? 1 : 0)) * (ROWS * (D + 2));

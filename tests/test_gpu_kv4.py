@@ -320,11 +320,13 @@ def test_lengths_beyond_the_table_and_queries_beyond_q_are_cut():
 
 def test_rows_behind_the_last_request_are_left():
     q, cache, table, lens, cu = setup([40, 9], [1, 1], 4, 2, 128, 16, seed=9)
-    want = run_attention(q, cache, table, lens, cu, 0.1, 64)
     pad = torch.cat([q, torch.full((5, 4, 128), float("nan"), dtype=torch.bfloat16)])
     out = torch.full((7, 4, 128), 3.0, dtype=torch.bfloat16, device="cuda")
     got = run_attention(pad, cache, table, lens, cu, 0.1, 64, out=out)
-    assert torch.equal(got[:2], want) and bool((got[2:] == 3.0).all())
+    # (the number of rows, padding included, chooses the height of the row
+    # blocks, so the sums' order may be another than without padding)
+    check(got[:2], q, cache, table, lens, cu, 0.1, 64)
+    assert bool((got[2:] == 3.0).all())
 
 
 def test_queries_as_columns_of_a_fused_projection():
