@@ -18,14 +18,6 @@
 
 namespace frag {
 
-// Codes of one 32-bit word (8 codes, low nibble first) as int8: 16 times the
-// odd codes and 16 times the even codes (a nibble at the top of a byte is the
-// signed code times 16).
-__device__ __forceinline__ void codes_s8(uint32_t w, uint32_t &odd, uint32_t &even) {
-    odd = w & 0xF0F0F0F0u;
-    even = (w * 16u) & 0xF0F0F0F0u;
-}
-
 // Codes of one 32-bit word as f16 pairs (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7), each code offset by 8 and all
 // times 2^-24.  A nibble XOR 8 is u = code + 8, and an f16 whose bits are a
 // small whole number u is the subnormal u 2^-24, exactly, which the matrix
@@ -37,11 +29,13 @@ __device__ __forceinline__ void codes_s8(uint32_t w, uint32_t &odd, uint32_t &ev
 constexpr float kCodeUnit = 1.0f / 16777216.0f;   // 2^-24
 
 // The masks are values that the compiler cannot see: as immediates the AND and
-// the XOR, one three-input operation between registers, become two.
+// the XOR, one three-input operation between registers, become two, and a
+// product by 16 becomes a shift, which the integer pipe has to run.
 struct CodeMasks {
-    uint32_t low, low8, high, high8;
+    uint32_t low, low8, high, high8, sixteen;
     __device__ __forceinline__ CodeMasks() {
         const uint32_t z = gridDim.z;   // 1
+        sixteen = 15u + z;
         low = 0x000F000Eu + z;
         low8 = 0x00080007u + z;
         high = 0x00F000EFu + z;
@@ -61,6 +55,14 @@ __device__ __forceinline__ void codes_f16(const CodeMasks &k, uint32_t w, uint32
     o[1] = and_xor(w, k.high, k.high8);
     o[2] = and_xor(w8, k.low, k.low8);
     o[3] = and_xor(w8, k.high, k.high8);
+}
+
+// Codes of one 32-bit word (8 codes, low nibble first) as int8: 16 times the
+// odd codes and 16 times the even codes (a nibble at the top of a byte is the
+// signed code times 16).
+__device__ __forceinline__ void codes_s8(const CodeMasks &k, uint32_t w, uint32_t &odd, uint32_t &even) {
+    odd = w & 0xF0F0F0F0u;
+    even = (w * k.sixteen) & 0xF0F0F0F0u;
 }
 
 // The codes as exact bf16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7): 0x4300
@@ -105,6 +107,23 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B: the same without a first summand.
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // The transpose of an 8 x 8 tile of 16-bit values held one row per 4 lanes.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -130,6 +149,16 @@ __device__ __forceinline__ float bf16_f32(uint16_t v) {
 
 __device__ __forceinline__ uint16_t f32_bf16(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// 16 bytes into shared memory (this thread's copies, in groups), or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ---------------------------------------------------------------- rotation

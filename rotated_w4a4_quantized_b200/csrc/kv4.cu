@@ -287,21 +287,25 @@ read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *_
 //   codes with up to 4 rows, else six; the offset's part of the
 //   outputs, -8 times the sum of the weights, comes out of one more product
 //   with a matrix of ones and is taken off before each tile.
-// P s_v is f16 relative to the largest exponent of s_v so far (powers of two;
-// outputs are rescaled when it grows, as they are when the maximum does):
-// 2^-11 relative for weights down to 2^-28 of the largest.
+// The softmax's reference is not the running maximum but within 2^8 of it: it
+// moves, and the outputs are rescaled, only when a score is more than 8 (log2)
+// above it, so most tiles need no maximum over their lanes.  P s_v is f16
+// relative to the largest exponent of s_v so far, in the same way: 2^-11
+// relative for weights down to 2^-20 of the reference, and 2^-31 of it off
+// below.
 //
 // Which keys of a 16-key block sit in which row of the product is free as
 // long as both products agree.  Row r holds key sigma(r), chosen so that both
 // the 16-byte reads of K and the 4 D/64-byte reads of V spread over the banks.
 //
 // Copies.  Each warp has its own place for a tile's keys and one for its
-// values (codes and scales, 64 (D + 4) bytes together), filled by bulk copies,
-// one per run of keys in a page, that complete on the warp's own barriers: no
-// warp waits for another inside a request.  The next tile's keys are requested
-// as soon as this one's scores are there, its values after the second product:
-// with 16 warps an SM a warp has several times the copy's latency until it
-// needs them, and registers, not bytes on the way, are what is short.
+// values (codes and scales, 64 (D + 4) bytes together), filled by its own
+// 16-byte asynchronous copies: no warp waits for another inside a request.
+// (Bulk copies take 25 instructions each, a lane at a time.)  The next tile's
+// keys are requested as soon as this one's scores are there, its values after
+// the second product: with 16 warps an SM a warp has several times the copy's
+// latency until it needs them, and registers, not bytes on the way, are what
+// is short.
 //
 // Work.  Units of one tile for one (request, head, row block) are laid out in
 // one line; CTA c takes units [c S, (c + 1) S), so ragged lengths load the
@@ -314,7 +318,10 @@ constexpr int kMaxCtas = 592;
 
 constexpr int kTile = 64;               // keys
 constexpr int kMinUnits = kAttnWarps;   // at least one tile a warp
-constexpr uint32_t kLeastExponent = 15;   // of a reference scale, so that 2^14 over it is a float
+constexpr uint32_t kLeastExponent = 15;   // of a reference scale, so that 2^kUnit over it is a float
+constexpr uint32_t kUnit = 6;             // weights are at most 2^kRoom 2^kUnit 2
+constexpr float kRoom = 8.0f;
+constexpr uint32_t kOnes = 0x3C003C00u;   // two f16
 
 struct AttnArgs {
     Cache c;
@@ -363,13 +370,6 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Contiguous bytes (16-byte aligned, a multiple of 16) into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
 // Output row r of a row block -> rotate back 16 channels a thread and store.
 __device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, int h, int row,
                                           int part, float (&x)[16], float total) {
@@ -400,8 +400,6 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     uint2 *qf = reinterpret_cast<uint2 *>(smem);
     uint8_t *stages = reinterpret_cast<uint8_t *>(qf + (HALF ? 1 : 2 * NT) * NW * 32);
     float *osum = reinterpret_cast<float *>(stages);  // [warps][ROWS][PITCH], once the tiles are done
-    __shared__ uint64_t bars[kAttnWarps][2];          // keys and values of a warp's tile
-    __shared__ int abort_flag;
     __shared__ float qs[ROWS];
     __shared__ int qmax[ROWS];
     __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS], wunit[kAttnWarps];
@@ -414,11 +412,6 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    if (tid == 0) abort_flag = 0;
-    if (lane == 0)
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&bars[warp][i]), 1);
-    ptx::fence_mbar_init();
-
     // ---- this CTA's part of the line of units
     const int chunk = (a.B + kAttnThreads - 1) / kAttnThreads;
     const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
@@ -462,11 +455,11 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     __syncthreads();
     int b = start_b;
     long long base = start_unit;        // first unit of request b
-    uint32_t parity = 0;                // of the warp's next tile
     const uint8_t *st = stages + warp * STAGE;
     const uint32_t st_s = ptx::smem_u32(st);
-    const uint32_t key_bar = ptx::smem_u32(&bars[warp][0]), value_bar = ptx::smem_u32(&bars[warp][1]);
     const uint16_t *sks = reinterpret_cast<const uint16_t *>(st + TILE * D), *svs = sks + TILE;
+    const int page_mask = (1 << a.c.page_shift) - 1, num_pages = static_cast<int>(a.c.num_pages);
+    const bool one_page = a.c.page_shift >= 6;   // a tile lies in one page
     const frag::CodeMasks masks;
     // this thread's row in a 16-key block, of its first scores
     const int key0 = sigma(g) + (HALF && t4 >= 2 ? 8 : 0);
@@ -476,11 +469,6 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     // HALF: the transposed weights of two keys -> (low, 0) and (high, 0) for
     // columns 0-3, (0, low) and (0, high) for columns 4-7
     const uint32_t pick_low = g < 4 ? 0x4410u : 0x1044u, pick_high = g < 4 ? 0x4432u : 0x3244u;
-    // keys of a tile in one page, the average bytes of a lane's copy, and the
-    // lanes that copy a whole tile
-    const int piece_shift = min(a.c.page_shift, 6), run_half = (D / 2 + 2) << (piece_shift - 1);
-    const uint32_t every_run = TILE >> piece_shift == 1 ? 3u : TILE >> piece_shift == 2 ? 15u : 255u;
-    const int page_mask = (1 << a.c.page_shift) - 1, num_pages = static_cast<int>(a.c.num_pages);   // keys of a tile in one page
 
     for (long long u = u0; u < u1;) {
         Request rq = request_of<ROWS>(a, b);
@@ -501,36 +489,62 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
         __syncthreads();                // the last request's shared data is done with
         const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
         // Request a tile's keys; its values are requested once the last
-        // tile's have been read.  Lane 2 p + i copies the codes (i = 0) or the
-        // scales of the p-th run of keys that lie in one page.
-        const int run = (lane >> 1) << piece_shift;
-        const int unit_bytes = (lane & 1) ? 2 : D / 2;              // of a key
-        const int64_t head_at = (static_cast<int64_t>(h) << a.c.page_shift) * unit_bytes;
-        const uint8_t *key_base = ((lane & 1) ? reinterpret_cast<const uint8_t *>(a.c.ks) : a.c.kc) + head_at;
-        const uint8_t *value_base = ((lane & 1) ? reinterpret_cast<const uint8_t *>(a.c.vs) : a.c.vc) + head_at;
-        const int page_bytes = (a.c.heads << a.c.page_shift) * unit_bytes;
-        int64_t run_at = -1;            // the run's place behind the base, -1: none
-        uint32_t runs = 0;              // lanes that copy
-        auto copy = [&](int i) {        // keys (0) or values (1)
-            const uint32_t bar = i ? value_bar : key_bar;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, __popc(runs) * run_half);
-            if (run_at >= 0)
-                bulk_load(((lane & 1) ? st_s + TILE * D + i * (TILE * 2) : st_s + i * (TILE * D / 2)) + run * unit_bytes,
-                          (i ? value_base : key_base) + run_at, unit_bytes << piece_shift, bar);
+        // tile's have been read.  A copy instruction takes KPI keys' codes,
+        // 16 bytes a lane; lanes 0-7 take the scales, 8 keys each.
+        constexpr int CPK = D / 32, KPI = 32 / CPK;
+        const int64_t head_at = static_cast<int64_t>(h) << a.c.page_shift;
+        int ids[NB];                    // pages of the tile's 16-key blocks, -1: none
+        int in_page = 0;                // the tile's first key in its page
+#pragma unroll
+        for (int i = 0; i < NB; ++i) ids[i] = -1;
+        auto copy = [&](const uint8_t *codes, const uint16_t *scales, int i) {   // keys (0) or values (1)
+            const uint32_t dst = st_s + i * (TILE * D / 2) + 16 * lane, sdst = st_s + TILE * D + i * (TILE * 2) + 16 * lane;
+            if (one_page) {
+                const int64_t row = (((static_cast<int64_t>(ids[0]) * a.c.heads) << a.c.page_shift) + head_at) + in_page;
+                const bool there = ids[0] >= 0;
+                const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
+#pragma unroll
+                for (int y = 0; y < TILE / KPI; ++y)
+                    frag::cp_async16_or_zero(dst + 512 * y, there ? src + 512 * y : src, there);
+                if (lane < 8) frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * lane : scales, there);
+            } else {
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk) {
+                    const int64_t row = (((static_cast<int64_t>(ids[blk]) * a.c.heads) << a.c.page_shift) + head_at) +
+                                        ((in_page + 16 * blk) & page_mask);
+                    const bool there = ids[blk] >= 0;
+                    const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
+#pragma unroll
+                    for (int y = 0; y < 16 / KPI; ++y)
+                        frag::cp_async16_or_zero(dst + (16 / KPI * blk + y) * 512, there ? src + 512 * y : src, there);
+                    if ((lane >> 1) == blk)
+                        frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * (lane & 1) : scales, there);
+                }
+            }
+            prep::cp_async_commit();
+        };
+        auto page_of = [&](int j0) {
+            int id = -1;
+            if (j0 < rq.len) {
+                id = table[j0 >> a.c.page_shift];
+                if (id < 0 || id >= num_pages) {
+                    if (lane == 0) page_error();
+                    id = -1;
+                }
+            }
+            return id;
         };
         auto request = [&](int tile) {
-            const int j0 = tile * TILE + run;
-            const bool want = run < TILE && j0 < rq.len;
-            const int id = want ? table[j0 >> a.c.page_shift] : -1;
-            const bool there = id >= 0 && id < num_pages;
-            if (want && !there) page_error();
-            run_at = there ? static_cast<int64_t>(id) * page_bytes + (j0 & page_mask) * unit_bytes : -1;
-            runs = __ballot_sync(0xFFFFFFFFu, there);
-            copy(0);
+            in_page = (tile * TILE) & page_mask;
+            if (one_page) ids[0] = page_of(tile * TILE);
+            else
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk) ids[blk] = page_of(tile * TILE + 16 * blk);
+            copy(a.c.kc, a.c.ks, 0);
         };
         if (tile0 + warp < tile1) {
             request(tile0 + warp);
-            copy(1);
+            copy(a.c.vc, a.c.vs, 1);
         }
         // ---- queries: rotate, scale to f16, lay out as B fragments
         for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
@@ -603,22 +617,30 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
             for (int j = 0; j < NW; ++j) qreg[j] = qf[j * 32 + lane];
 
         float o[MT][NT][4] = {};
-        float m[NT][2], l[NT][2];
+        // reference of the softmax and how far above it (log2) a score may be
+        // before the reference moves: not at all until there is one
+        float m[NT][2], room[NT][2], l[NT][2];
         uint32_t ref = kLeastExponent;  // the values' scales are taken relative to 2^(ref - 127 - 14)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                m[nt][x] = -INFINITY;
+                m[nt][x] = 0.0f;
+                room[nt][x] = -INFINITY;
                 l[nt][x] = 0.0f;
             }
 
         for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
             const int k0 = tile * TILE;
-            const uint32_t here = runs;
-            // every query sees every key of the tile
-            const bool all = here == every_run && k0 + TILE - 1 <= least;
-            if (!ptx::mbar_wait(key_bar, parity, &abort_flag)) break;
+            // 16-key blocks that are there; whether every query sees every key
+            uint32_t here = 0;
+            if (one_page) here = ids[0] >= 0 ? (1u << NB) - 1 : 0u;
+            else
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk) here |= (ids[blk] >= 0 ? 1u : 0u) << blk;
+            const bool all = here == (1u << NB) - 1 && k0 + TILE - 1 <= least;
+            frag::cp_async_wait<1>();   // the keys are there, the values may be on their way
+            __syncwarp();
             float s[NB][NT][NS];
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
@@ -634,31 +656,38 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                         reinterpret_cast<uint4 *>(kb)[i] = *reinterpret_cast<const uint4 *>(pb + 64 * i + 16 * t4);
                     }
                 }
-                int high[NT][4] = {}, low[HALF ? 1 : NT][4] = {};
+                int high[NT][4], low[HALF ? 1 : NT][4];
 #pragma unroll
                 for (int j = 0; j < NW; j += 2) {
                     uint32_t ao[2], ae[2], bo[2], be[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        frag::codes_s8(ka[j + y], ao[y], ae[y]);
-                        frag::codes_s8(kb[j + y], bo[y], be[y]);
+                        frag::codes_s8(masks, ka[j + y], ao[y], ae[y]);
+                        frag::codes_s8(masks, kb[j + y], bo[y], be[y]);
                     }
                     if constexpr (HALF) {
-                        frag::mma_s8(high[0], ao[0], bo[0], ao[1], bo[1], qreg[j].x, qreg[j + 1].x);
+                        if (j == 0) frag::mma_s8_first(high[0], ao[0], bo[0], ao[1], bo[1], qreg[j].x, qreg[j + 1].x);
+                        else frag::mma_s8(high[0], ao[0], bo[0], ao[1], bo[1], qreg[j].x, qreg[j + 1].x);
                         frag::mma_s8(high[0], ae[0], be[0], ae[1], be[1], qreg[j].y, qreg[j + 1].y);
                     } else {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint2 *q = qf + (nt * NW + j) * 64 + lane;
                             const uint2 h0 = q[0], l0 = q[32], h1 = q[64], l1 = q[96];
-                            frag::mma_s8(high[nt], ao[0], bo[0], ao[1], bo[1], h0.x, h1.x);
-                            frag::mma_s8(low[nt], ao[0], bo[0], ao[1], bo[1], l0.x, l1.x);
+                            if (j == 0) {
+                                frag::mma_s8_first(high[nt], ao[0], bo[0], ao[1], bo[1], h0.x, h1.x);
+                                frag::mma_s8_first(low[nt], ao[0], bo[0], ao[1], bo[1], l0.x, l1.x);
+                            } else {
+                                frag::mma_s8(high[nt], ao[0], bo[0], ao[1], bo[1], h0.x, h1.x);
+                                frag::mma_s8(low[nt], ao[0], bo[0], ao[1], bo[1], l0.x, l1.x);
+                            }
                             frag::mma_s8(high[nt], ae[0], be[0], ae[1], be[1], h0.y, h1.y);
                             frag::mma_s8(low[nt], ae[0], be[0], ae[1], be[1], l0.y, l1.y);
                         }
                     }
                 }
-                // 256 high + low, exact in 32 bits, and the scores in units of log2
+                // 256 high + low, exact in 32 bits; scores in units of log2,
+                // less the reference
                 const float ska = frag::bf16_f32(sks[16 * blk + key0]);
                 if constexpr (HALF) {
                     // columns 0-3 have the high bytes' sums and columns 4-7 the
@@ -669,7 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                         const int mine = first ? high[0][x] : high[0][2 + x];
                         const int theirs = __shfl_xor_sync(0xFFFFFFFFu, first ? high[0][2 + x] : high[0][x], 2);
                         const int sum = mine * weight_mine + theirs * weight_theirs;
-                        s[blk][0][x] = static_cast<float>(sum) * (ska * cs[0][x]);
+                        s[blk][0][x] = fmaf(static_cast<float>(sum), ska * cs[0][x], -m[0][x]);
                     }
                 } else {
                     const float skb = frag::bf16_f32(sks[16 * blk + key0 + 8]);
@@ -677,18 +706,21 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            s[blk][nt][x] = static_cast<float>(256 * high[nt][x] + low[nt][x]) * ((x < 2 ? ska : skb) * cs[nt][x & 1]);
+                            s[blk][nt][x] = fmaf(static_cast<float>(256 * high[nt][x] + low[nt][x]),
+                                                 (x < 2 ? ska : skb) * cs[nt][x & 1], -m[nt][x & 1]);
                 }
             }
             __syncwarp();               // the keys have been read
             const bool more = tile + kAttnWarps < tile1;
             if (more) request(tile + kAttnWarps);
+            else prep::cp_async_commit();   // an empty group: the counts stay
             if (!all) {
+                asm volatile("");       // a branch: few tiles take it
                 // hidden keys are -inf whatever they hold
 #pragma unroll
                 for (int blk = 0; blk < NB; ++blk) {
                     const int ja = k0 + 16 * blk + key0;
-                    const bool there = (here >> (2 * ((16 * blk) >> piece_shift))) & 1;
+                    const bool there = (here >> blk) & 1;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -696,61 +728,85 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                             if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) s[blk][nt][x] = -INFINITY;
                 }
             }
-            // ---- running maximum and sum
-            float mul[NT][2];
+            frag::cp_async_wait<1>();   // the values are there, the next keys may be on their way
+            __syncwarp();
+            // ---- does a score or a value's scale leave the reference's room?
             bool turn = false;
+            const uint32_t two = reinterpret_cast<const uint32_t *>(svs)[lane];
+            uint32_t scale_bits = max(two & 0xFFFFu, two >> 16);
+            if (!all) {
+                asm volatile("");
+                // hidden and infinite scales do not count
+                const bool there = (here >> (lane >> 3)) & 1;
+                const uint32_t lo = two & 0xFFFFu, hi = two >> 16;
+                scale_bits = max(there && k0 + 2 * lane < rq.len && lo < 0x7F80u ? lo : 0u,
+                                 there && k0 + 2 * lane + 1 < rq.len && hi < 0x7F80u ? hi : 0u);
+            }
+            turn = scale_bits >= (ref + 1) << 7;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float top = m[nt][x];
+                    float top = s[0][nt][x];
 #pragma unroll
                     for (int blk = 0; blk < NB; ++blk) {
-                        if constexpr (HALF) top = fmaxf(top, s[blk][nt][x]);
-                        else top = prep::max3(top, s[blk][nt][x], s[blk][nt][2 + x]);
+                        if constexpr (!HALF) top = prep::max3(top, s[blk][nt][x], s[blk][nt][2 + x]);
+                        else if (blk & 1) top = prep::max3(top, s[blk][nt][x], s[blk ^ 1][nt][x]);
                     }
-                    for (int k = HALF ? 2 : 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-                    const float safe = top == -INFINITY ? 0.0f : top;
-                    mul[nt][x] = ex2(m[nt][x] - safe);
-                    turn |= top != m[nt][x];
-                    m[nt][x] = top;
-                    l[nt][x] *= mul[nt][x];
+                    turn |= top > room[nt][x];
+                }
+            if (__any_sync(0xFFFFFFFFu, turn)) {
+                const uint32_t exponent = min(__reduce_max_sync(0xFFFFFFFFu, scale_bits) >> 7, 254u);
+                float shift = 1.0f;
+                if (exponent > ref) {
+                    shift = exponent - ref < 127 ? __uint_as_float((127 - (exponent - ref)) << 23) : 0.0f;
+                    ref = exponent;
+                }
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float mul[2];
 #pragma unroll
-                        for (int y = 0; y < NS; y += 2) {
-                            const float p = ex2(s[blk][nt][y + x] - safe);
-                            l[nt][x] += p;
-                            s[blk][nt][y + x] = p;
+                    for (int x = 0; x < 2; ++x) {
+                        float top = s[0][nt][x];
+#pragma unroll
+                        for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                            for (int y = 0; y < NS; y += 2) top = fmaxf(top, s[blk][nt][y + x]);
+                        for (int k = HALF ? 2 : 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+                        mul[x] = 1.0f;
+                        if (top > room[nt][x]) {
+                            m[nt][x] += top;
+                            room[nt][x] = kRoom;
+                            mul[x] = ex2(-top);      // of nothing, at first
+                            if (l[nt][x] == 0.0f) mul[x] = 0.0f;
+                            l[nt][x] *= mul[x];
+#pragma unroll
+                            for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                                for (int y = 0; y < NS; y += 2) s[blk][nt][y + x] -= top;
                         }
+                        mul[x] *= shift;
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= mul[x & 1];
                 }
-            if (!ptx::mbar_wait(value_bar, parity, &abort_flag)) break;
-            parity ^= 1;
-            // the largest exponent of the values' scales so far; hidden and
-            // infinite ones do not count
-            uint32_t top_bits = 0;
-            {
-                const uint32_t two = reinterpret_cast<const uint32_t *>(svs)[lane];
-                uint32_t lo = two & 0xFFFFu, hi = two >> 16;
-                if (!all) {
-                    const bool there = (here >> (2 * ((2 * lane) >> piece_shift))) & 1;
-                    if (!there || k0 + 2 * lane >= rq.len || lo >= 0x7F80u) lo = 0;
-                    if (!there || k0 + 2 * lane + 1 >= rq.len || hi >= 0x7F80u) hi = 0;
-                }
-                top_bits = max(lo, hi);
             }
-            const uint32_t exponent = min(__reduce_max_sync(0xFFFFFFFFu, top_bits) >> 7, 254u);
-            float shift = 1.0f;
-            if (exponent > ref) {
-                turn = true;
-                shift = exponent - ref < 127 ? __uint_as_float((127 - (exponent - ref)) << 23) : 0.0f;
-                ref = exponent;
-            }
-            const float unit = __uint_as_float((127 + 14 + 127 - ref) << 23);   // 2^14 over the reference
+            const float unit = __uint_as_float((127 + kUnit + 127 - ref) << 23);   // 2^kUnit over the reference
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < NS; ++x) {
+                        s[blk][nt][x] = ex2(s[blk][nt][x]);
+                        l[nt][x & 1] += s[blk][nt][x];
+                    }
             // ---- weights of the values, as f16 fragments, and their sums
             // HALF: p[blk][0][..] are the keys of rows 0-7 (two of them) and rows 8-15
             uint32_t p[NB][NT][HALF ? 4 : 2];
-            float psum[NT][4] = {};
+            float psum[NT][4];
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
                 const float sva = unit * frag::bf16_f32(svs[16 * blk + key0]);
@@ -760,9 +816,11 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                     float w[NS];
 #pragma unroll
                     for (int x = 0; x < NS; ++x) w[x] = s[blk][nt][x] * (x < 2 ? sva : svb);
-                    if (!all) {         // a hidden key's scale may be anything
+                    if (!all) {
+                        asm volatile("");
+                        // a hidden key's scale may be anything
                         const int ja = k0 + 16 * blk + key0;
-                        const bool there = (here >> (2 * ((16 * blk) >> piece_shift))) & 1;
+                        const bool there = (here >> blk) & 1;
 #pragma unroll
                         for (int x = 0; x < NS; ++x)
                             if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) w[x] = 0.0f;
@@ -783,16 +841,9 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                     }
 #pragma unroll
                     for (int y = 0; y < (HALF ? 4 : 2); y += 2)
-                        frag::mma_f16(psum[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[blk][nt][y], p[blk][nt][y + 1]);
+                        if (blk == 0 && y == 0) frag::mma_f16_first(psum[nt], kOnes, kOnes, kOnes, kOnes, p[blk][nt][y], p[blk][nt][y + 1]);
+                        else frag::mma_f16(psum[nt], kOnes, kOnes, kOnes, kOnes, p[blk][nt][y], p[blk][nt][y + 1]);
                 }
-            }
-            if (__any_sync(0xFFFFFFFFu, turn)) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= shift * mul[nt][x & 1];
             }
             // the codes' offset of 8, taken off tile by tile so that it never
             // grows far beyond the sums it is part of
@@ -861,8 +912,10 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                 }
             }
             __syncwarp();               // the values have been read
-            if (more) copy(1);
+            if (more) copy(a.c.vc, a.c.vs, 1);
+            else prep::cp_async_commit();
         }
+        frag::cp_async_wait<0>();
 
         // ---- join the warps
         __syncthreads();                // every tile is done
@@ -872,11 +925,11 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
             for (int x = 0; x < 2; ++x) {
                 for (int k = HALF ? 2 : 4; k < 32; k <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], k);
                 if (g == 0) {
-                    wm[warp][8 * nt + col0 + x] = m[nt][x];
+                    wm[warp][8 * nt + col0 + x] = room[nt][x] == -INFINITY ? -INFINITY : m[nt][x];
                     wl[warp][8 * nt + col0 + x] = l[nt][x];
                 }
             }
-        if (lane == 0) wunit[warp] = __uint_as_float((ref - 14) << 23);
+        if (lane == 0) wunit[warp] = __uint_as_float((ref - kUnit) << 23);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -925,7 +978,6 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                 for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
         }
-        ptx::fence_proxy_async_smem();  // these reads and writes come before the next copies into the stages
         if (!whole && seg_u0 >= u0 && tid == 0)
             a.desc[blockIdx.x] = make_int4(static_cast<int>((seg_u1 - 1) / share), b, h, rb);
         u = seg_u0 + tile1;
@@ -1195,6 +1247,10 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
                seq_lens, cu_q, static_cast<int>(B), scale * 1.4426950408889634f, static_cast<int4 *>(workspace),
                reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(ctas * sizeof(int4))),
                static_cast<uint16_t *>(out_bf16)};
+    if (!cache->num_pages) {   // copies of no bytes still name an address
+        a.c.kc = a.c.vc = static_cast<uint8_t *>(const_cast<void *>(q_bf16));
+        a.c.ks = a.c.vs = static_cast<uint16_t *>(const_cast<void *>(q_bf16));
+    }
     const int sms = host::g_dev[dev].num_sms;
     auto go = [&](auto d) {
         constexpr int DIM = decltype(d)::value;

@@ -92,15 +92,6 @@ struct Args {
     int wait;                // a rotation kernel comes before this one
 };
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // NT: token columns / 8.  SG: scale group.
 template <int NT, int SG>
 __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
@@ -130,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
                 const int r = (lane >> 3) + 4 * i, c = lane & 7;
                 const int byte = stage * (kStage / 2) + 16 * c;
                 const bool live = r < tile_rows && byte < a.K / 2;
-                cp_async16_or_zero(ring + slot * kStageBytes + r * 128 + ((c ^ (r & 7)) << 4),
+                frag::cp_async16_or_zero(ring + slot * kStageBytes + r * 128 + ((c ^ (r & 7)) << 4),
                                    live ? wrow + static_cast<int64_t>(r) * (a.K / 2) + byte : a.qw, live);
             }
         }
@@ -179,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
                 sc[1][i] = next[1][i];
             }
             load_scales(stage + parts, next);
-            cp_async_wait<kDepth - 1>();
+            frag::cp_async_wait<kDepth - 1>();
             __syncwarp();
             const uint8_t *src = reinterpret_cast<const uint8_t *>(smem) + warp * (kDepth * kStageBytes) + slot * kStageBytes + 128 * g + 4 * t4;
             const uint4 *xs = act + ((stage - s0) * (kStage / 8) + t4) * tokens + g;
@@ -213,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
             slot = (slot + 1) % kDepth;
         }
     }
-    cp_async_wait<0>();
+    frag::cp_async_wait<0>();
 
     // ---- join the parts of K in their order, add the bias, round
     __syncthreads();

@@ -109,10 +109,11 @@ def attention(q, cache, table, lens, cu_q, scale, group, dead=()):
                     allow[a + i, hq] = e * (p @ vv.abs()).norm() + 2.0 ** -8 * out[a + i, hq].norm()
                     # the offset of the values' codes comes and goes in every
                     # tile: 8 sum p s_v, off by an ulp (2^-23) in each of five
-                    # steps, and weights below the f16 range (2^-34 of the
-                    # largest scale each), in each of D values
+                    # steps, and weights below the f16 range (half a step,
+                    # 2^-25 of a unit that is 2^-6 of the reference, times
+                    # twice the largest scale), in each of D values
                     sv = ks_rows(vs, row, n, h)[seen]
-                    allow[a + i, hq] += D ** 0.5 * (8 * 5 * 2.0 ** -23 * float(p @ sv) + 7 * 2.0 ** -34 * float(sv.max()) * len(sv))
+                    allow[a + i, hq] += D ** 0.5 * (8 * 5 * 2.0 ** -23 * float(p @ sv) + 7 * 2.0 ** -30 * float(sv.max()) * len(sv))
     return out, allow
 
 
