@@ -383,6 +383,18 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, 
 }
 
 template <int D, int ROWS>
+__host__ __device__ constexpr bool outputs_beside() {
+    return kAttnWarps * (kTile * (D + 4) + ROWS * (D + 4) * 4) <= 110 * 1024;
+}
+
+// One request's part of a CTA's work: a head, a row block and tiles.
+struct Segment {
+    int b, h, rb, tile0, tile1;
+    long long u0, u1;           // its first unit and the one behind its last, of all CTAs
+    Request rq;
+};
+
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) attention_kernel(AttnArgs a) {
     constexpr bool HALF = ROWS == 4;    // the columns hold the two bytes of four queries
     constexpr int NT = HALF ? 1 : ROWS / 8;
@@ -399,7 +411,11 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     // lanes], else [NT][NW][high, low byte][32 lanes]
     uint2 *qf = reinterpret_cast<uint2 *>(smem);
     uint8_t *stages = reinterpret_cast<uint8_t *>(qf + (HALF ? 1 : 2 * NT) * NW * 32);
-    float *osum = reinterpret_cast<float *>(stages);  // [warps][ROWS][PITCH], once the tiles are done
+    // outputs of the warps [warps][ROWS][PITCH]: beside the stages, so that the
+    // next request's first tiles come in while this one's outputs are joined,
+    // or in their place where that leaves two CTAs to an SM
+    constexpr bool BESIDE = outputs_beside<D, ROWS>();
+    float *osum = reinterpret_cast<float *>(stages + (BESIDE ? kAttnWarps * STAGE : 0));
     __shared__ float qs[ROWS];
     __shared__ int qmax[ROWS];
     __shared__ float wm[kAttnWarps][ROWS], wl[kAttnWarps][ROWS], wunit[kAttnWarps];
@@ -412,6 +428,8 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
+    ptx::launch_dependents();           // the combining CTAs take the places of those that are done
+    ptx::grid_dependency_wait();
     // ---- this CTA's part of the line of units
     const int chunk = (a.B + kAttnThreads - 1) / kAttnThreads;
     const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
@@ -433,7 +451,9 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    long long share = (total + gridDim.x - 1) / gridDim.x;
+    long long share = total < (1ll << 31)
+                          ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
+                          : (total + gridDim.x - 1) / static_cast<long long>(gridDim.x);
     if (share < kMinUnits) share = kMinUnits;
     const long long u0 = share * blockIdx.x;
     const long long u1 = min(u0 + share, total);
@@ -470,90 +490,119 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     // columns 0-3, (0, low) and (0, high) for columns 4-7
     const uint32_t pick_low = g < 4 ? 0x4410u : 0x1044u, pick_high = g < 4 ? 0x4432u : 0x3244u;
 
-    for (long long u = u0; u < u1;) {
-        Request rq = request_of<ROWS>(a, b);
-        long long n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
-        while (u >= base + n) {
+    auto locate = [&](long long u) {
+        Segment sg;
+        sg.rq = request_of<ROWS>(a, b);
+        long long n = static_cast<long long>(sg.rq.tiles) * sg.rq.blocks * a.c.heads;
+        while (u >= base + n && b + 1 < a.B) {
             base += n;
-            if (++b >= a.B) return;     // lengths that changed under the kernel
-            rq = request_of<ROWS>(a, b);
-            n = static_cast<long long>(rq.tiles) * rq.blocks * a.c.heads;
+            sg.rq = request_of<ROWS>(a, ++b);
+            n = static_cast<long long>(sg.rq.tiles) * sg.rq.blocks * a.c.heads;
         }
-        const int seg = static_cast<int>((u - base) / rq.tiles);
-        const int tile0 = static_cast<int>((u - base) % rq.tiles);
-        const long long seg_u0 = base + static_cast<long long>(seg) * rq.tiles, seg_u1 = seg_u0 + rq.tiles;
-        const int tile1 = static_cast<int>(min(u1, seg_u1) - seg_u0);
-        const int h = seg / rq.blocks, rb = seg % rq.blocks;
-        const int row0 = rb * ROWS;
-
-        __syncthreads();                // the last request's shared data is done with
-        const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
-        // Request a tile's keys; its values are requested once the last
-        // tile's have been read.  A copy instruction takes KPI keys' codes,
-        // 16 bytes a lane; lanes 0-7 take the scales, 8 keys each.
-        constexpr int CPK = D / 32, KPI = 32 / CPK;
-        const int64_t head_at = static_cast<int64_t>(h) << a.c.page_shift;
-        int ids[NB];                    // pages of the tile's 16-key blocks, -1: none
-        int in_page = 0;                // the tile's first key in its page
-#pragma unroll
-        for (int i = 0; i < NB; ++i) ids[i] = -1;
-        auto copy = [&](const uint8_t *codes, const uint16_t *scales, int i) {   // keys (0) or values (1)
-            const uint32_t dst = st_s + i * (TILE * D / 2) + 16 * lane, sdst = st_s + TILE * D + i * (TILE * 2) + 16 * lane;
-            if (one_page) {
-                const int64_t row = (((static_cast<int64_t>(ids[0]) * a.c.heads) << a.c.page_shift) + head_at) + in_page;
-                const bool there = ids[0] >= 0;
-                const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
-#pragma unroll
-                for (int y = 0; y < TILE / KPI; ++y)
-                    frag::cp_async16_or_zero(dst + 512 * y, there ? src + 512 * y : src, there);
-                if (lane < 8) frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * lane : scales, there);
-            } else {
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk) {
-                    const int64_t row = (((static_cast<int64_t>(ids[blk]) * a.c.heads) << a.c.page_shift) + head_at) +
-                                        ((in_page + 16 * blk) & page_mask);
-                    const bool there = ids[blk] >= 0;
+        const long long at = min(u - base, n - 1);   // (n is 0 only if lengths change under the kernel)
+        const int seg = n < 1 ? 0 : at < (1ll << 31) ? static_cast<int>(static_cast<unsigned>(at) / sg.rq.tiles)
+                                                     : static_cast<int>(at / sg.rq.tiles);
+        sg.b = b;
+        sg.u0 = base + static_cast<long long>(seg) * sg.rq.tiles;
+        sg.u1 = sg.u0 + sg.rq.tiles;
+        sg.tile0 = static_cast<int>(max(u - sg.u0, 0ll));
+        sg.tile1 = static_cast<int>(min(u1, sg.u1) - sg.u0);
+        const int blocks = max(sg.rq.blocks, 1);
+        sg.h = seg / blocks;
+        sg.rb = seg % blocks;
+        return sg;
+    };
+            // Request a tile's keys; its values are requested once the last
+            // tile's have been read.  A copy instruction takes KPI keys' codes,
+            // 16 bytes a lane; lanes 0-7 take the scales, 8 keys each.
+            constexpr int CPK = D / 32, KPI = 32 / CPK;
+                    int ids[NB];                    // pages of the tile's 16-key blocks, -1: none
+            int in_page = 0;                // the tile's first key in its page
+    #pragma unroll
+            for (int i = 0; i < NB; ++i) ids[i] = -1;
+            auto copy = [&](int h, const uint8_t *codes, const uint16_t *scales, int i) {   // keys (0) or values (1)
+                const uint32_t dst = st_s + i * (TILE * D / 2) + 16 * lane, sdst = st_s + TILE * D + i * (TILE * 2) + 16 * lane;
+                if (one_page) {
+                    const int64_t row = ((static_cast<int64_t>(ids[0]) * a.c.heads + h) << a.c.page_shift) + in_page;
+                    const bool there = ids[0] >= 0;
                     const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
-#pragma unroll
-                    for (int y = 0; y < 16 / KPI; ++y)
-                        frag::cp_async16_or_zero(dst + (16 / KPI * blk + y) * 512, there ? src + 512 * y : src, there);
-                    if ((lane >> 1) == blk)
-                        frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * (lane & 1) : scales, there);
+    #pragma unroll
+                    for (int y = 0; y < TILE / KPI; ++y)
+                        frag::cp_async16_or_zero(dst + 512 * y, there ? src + 512 * y : src, there);
+                    if (lane < 8) frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * lane : scales, there);
+                } else {
+    #pragma unroll
+                    for (int blk = 0; blk < NB; ++blk) {
+                        const int64_t row = ((static_cast<int64_t>(ids[blk]) * a.c.heads + h) << a.c.page_shift) +
+                                            ((in_page + 16 * blk) & page_mask);
+                        const bool there = ids[blk] >= 0;
+                        const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
+    #pragma unroll
+                        for (int y = 0; y < 16 / KPI; ++y)
+                            frag::cp_async16_or_zero(dst + (16 / KPI * blk + y) * 512, there ? src + 512 * y : src, there);
+                        if ((lane >> 1) == blk)
+                            frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * (lane & 1) : scales, there);
+                    }
                 }
-            }
-            prep::cp_async_commit();
-        };
-        auto page_of = [&](int j0) {
-            int id = -1;
-            if (j0 < rq.len) {
-                id = table[j0 >> a.c.page_shift];
-                if (id < 0 || id >= num_pages) {
-                    if (lane == 0) page_error();
-                    id = -1;
+                prep::cp_async_commit();
+            };
+            auto page_of = [&](const Segment &sg, int j0) {
+                int id = -1;
+                if (j0 < sg.rq.len) {
+                    id = a.table[sg.b * a.max_pages + (j0 >> a.c.page_shift)];
+                    if (id < 0 || id >= num_pages) {
+                        if (lane == 0) page_error();
+                        id = -1;
+                    }
                 }
-            }
-            return id;
-        };
-        auto request = [&](int tile) {
-            in_page = (tile * TILE) & page_mask;
-            if (one_page) ids[0] = page_of(tile * TILE);
-            else
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk) ids[blk] = page_of(tile * TILE + 16 * blk);
-            copy(a.c.kc, a.c.ks, 0);
-        };
-        if (tile0 + warp < tile1) {
-            request(tile0 + warp);
-            copy(a.c.vc, a.c.vs, 1);
+                return id;
+            };
+            auto request = [&](const Segment &sg, int tile) {
+                in_page = (tile * TILE) & page_mask;
+                if (one_page) ids[0] = page_of(sg, tile * TILE);
+                else
+    #pragma unroll
+                    for (int blk = 0; blk < NB; ++blk) ids[blk] = page_of(sg, tile * TILE + 16 * blk);
+                copy(sg.h, a.c.kc, a.c.ks, 0);
+            };
+            // The first of a segment's tiles, and this thread's queries of it.
+    uint4 raw[2];
+    auto query_at = [&](const Segment &sg, int i) -> const uint16_t * {
+        const int row = sg.rb * ROWS + i / LANES, qi = row / a.G;
+        if (i >= ROWS * LANES || qi >= sg.rq.nq) return nullptr;
+        return a.q + (static_cast<int64_t>(sg.rq.q0) + qi) * a.ldq + static_cast<int64_t>(sg.h * a.G + row % a.G) * D + 16 * (i % LANES);
+    };
+    auto load_query = [&](const Segment &sg, int i) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(query_at(sg, i));
+        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+        if (p) {
+            raw[0] = p[0];
+            raw[1] = p[1];
         }
-        // ---- queries: rotate, scale to f16, lay out as B fragments
+    };
+    auto start = [&](const Segment &sg) {
+        load_query(sg, tid);
+        if (sg.tile0 + warp < sg.tile1) {
+            request(sg, sg.tile0 + warp);
+            copy(sg.h, a.c.vc, a.c.vs, 1);
+        }
+    };
+
+    Segment next = locate(u0);
+    start(next);
+    for (bool last = false; !last;) {
+        const Segment sg = next;
+        const Request &rq = sg.rq;
+        const int tile0 = sg.tile0, tile1 = sg.tile1, h = sg.h, row0 = sg.rb * ROWS;
+        // ---- queries: rotate, round to 16 bits, lay out as B fragments
         for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
             const int i = i0 + tid;
             const int r = i / LANES, part = i % LANES;
-            const int qi = (row0 + r) / a.G, hd = h * a.G + (row0 + r) % a.G;
-            const bool live = r < ROWS && qi < rq.nq;
-            float x[16] = {};
-            if (live) frag::load16(a.q + (static_cast<int64_t>(rq.q0) + qi) * a.ldq + static_cast<int64_t>(hd) * D + 16 * part, x);
+            const int qi = (row0 + r) / a.G;
+            if (i0) load_query(sg, i);
+            float x[16];
+            frag::unpack_bf16x8(raw[0], x);
+            frag::unpack_bf16x8(raw[1], x + 8);
             frag::rotate16(x, a.c.group == 256);
             const uint32_t amax = frag::absmax_bits(x, LANES);
             // 16-bit whole numbers, the row's largest at 32000; rows below
@@ -712,7 +761,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
             }
             __syncwarp();               // the keys have been read
             const bool more = tile + kAttnWarps < tile1;
-            if (more) request(tile + kAttnWarps);
+            if (more) request(sg, tile + kAttnWarps);
             else prep::cp_async_commit();   // an empty group: the counts stay
             if (!all) {
                 asm volatile("");       // a branch: few tiles take it
@@ -912,13 +961,19 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                 }
             }
             __syncwarp();               // the values have been read
-            if (more) copy(a.c.vc, a.c.vs, 1);
+            if (more) copy(h, a.c.vc, a.c.vs, 1);
             else prep::cp_async_commit();
         }
         frag::cp_async_wait<0>();
+        const long long end = sg.u0 + tile1;
+        last = end >= u1;
 
         // ---- join the warps
-        __syncthreads();                // every tile is done
+        if constexpr (!BESIDE) __syncthreads();   // every tile is done
+        if (!last) {
+            next = locate(end);
+            if constexpr (BESIDE) start(next);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -942,8 +997,8 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                         o[i][nt][x] * (second_nibble(i, x) ? 1.0f / (16.0f * frag::kCodeUnit) : 1.0f / frag::kCodeUnit);
                 }
         __syncthreads();
-        const bool whole = seg_u0 >= u0 && seg_u1 <= u1;
-        float *part_out = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (seg_u0 >= u0 ? 1 : 0)) * (ROWS * (D + 2));
+        const bool whole = sg.u0 >= u0 && sg.u1 <= u1;
+        float *part_out = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (sg.u0 >= u0 ? 1 : 0)) * (ROWS * (D + 2));
         for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
             const int i = i0 + tid;
             const int r = min(i / LANES, ROWS - 1), part = i % LANES;
@@ -978,51 +1033,80 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                 for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
         }
-        if (!whole && seg_u0 >= u0 && tid == 0)
-            a.desc[blockIdx.x] = make_int4(static_cast<int>((seg_u1 - 1) / share), b, h, rb);
-        u = seg_u0 + tile1;
+        if (!whole && sg.u0 >= u0 && tid == 0)
+            a.desc[blockIdx.x] = make_int4(static_cast<int>((sg.u1 - 1) / share), sg.b, h, sg.rb);
+        if constexpr (!BESIDE) {
+            __syncthreads();            // the outputs have been read
+            if (!last) start(next);
+        }
     }
 }
 
 // CTA c joins the parts of the request that CTA c of attention_kernel began
-// and did not end.
+// and did not end: 16 channels of a row a thread, the parts dealt out to the
+// groups of ROWS D / 16 threads that the CTA has, which are joined at the end.
+constexpr int kCombineThreads = 256;
+
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kAttnThreads) combine_kernel(AttnArgs a) {
-    constexpr int LANES = D / 16;
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
+    constexpr int LANES = D / 16, USED = ROWS * LANES, WIDTH = USED < 32 ? 32 : USED, GROUPS = kCombineThreads / WIDTH;
+    static_assert(WIDTH % 32 == 0 && WIDTH <= kCombineThreads, "whole warps a group");
+    __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][4][WIDTH];
+    __shared__ float totals[GROUPS > 1 ? GROUPS - 1 : 1][WIDTH];
     ptx::grid_dependency_wait();
     const int4 d = a.desc[blockIdx.x];
     if (d.x < 0) return;
     const Request rq = request_of<ROWS>(a, d.y);
-    for (int i0 = 0; i0 < ROWS * LANES; i0 += kAttnThreads) {
-        const int i = i0 + static_cast<int>(threadIdx.x);
-        const int r = min(i / LANES, ROWS - 1), part = i % LANES;
-        float x[16] = {}, sum = 0.0f, top = -INFINITY;
-        for (int c = blockIdx.x; c <= d.x; ++c) {
-            const float *p = a.parts + (2 * static_cast<int64_t>(c) + (c == static_cast<int>(blockIdx.x) ? 1 : 0)) * (ROWS * (D + 2));
-            const float mc = p[2 * r], lc = p[2 * r + 1];
-            const float next = fmaxf(top, mc);
-            const float safe = next == -INFINITY ? 0.0f : next;
-            const float fo = ex2(top - safe), fn = ex2(mc - safe);
-            top = next;
-            sum = sum * fo + lc * fn;
-            const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
+    const int i = threadIdx.x % WIDTH, group = threadIdx.x / WIDTH, r = min(i / LANES, ROWS - 1), part = i % LANES;
+    const int c0 = blockIdx.x, count = d.x - c0 + 1;
+    auto at = [&](int k) {   // the k-th part: the first is its CTA's second
+        return a.parts + (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * (ROWS * (D + 2));
+    };
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < count; ++k) top = fmaxf(top, at(k)[2 * r]);
+    const float safe = top == -INFINITY ? 0.0f : top;
+    float x[16] = {}, sum = 0.0f;
+#pragma unroll 4
+    for (int k = group; k < count; k += GROUPS) {
+        const float *p = at(k);
+        const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * r);
+        const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
+        const float4 y0 = src[0], y1 = src[1], y2 = src[2], y3 = src[3];
+        const float f = ex2(ml.x - safe);
+        sum += f * ml.y;
+        const float y[16] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w, y2.x, y2.y, y2.z, y2.w, y3.x, y3.y, y3.z, y3.w};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] += f * y[e];
+    }
+    if constexpr (GROUPS > 1) {
+        if (group) {
+            totals[group - 1][i] = sum;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[group - 1][e][i] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        }
+        __syncthreads();
+        if (group) return;
+        for (int k = 0; k < GROUPS - 1; ++k) {
+            sum += totals[k][i];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float4 y = src[e];
-                x[4 * e] = x[4 * e] * fo + y.x * fn;
-                x[4 * e + 1] = x[4 * e + 1] * fo + y.y * fn;
-                x[4 * e + 2] = x[4 * e + 2] * fo + y.z * fn;
-                x[4 * e + 3] = x[4 * e + 3] * fo + y.w * fn;
+                const float4 y = sums[k][e][i];
+                x[4 * e] += y.x;
+                x[4 * e + 1] += y.y;
+                x[4 * e + 2] += y.z;
+                x[4 * e + 3] += y.w;
             }
         }
-        store_row(a, rq, d.z, i < ROWS * LANES ? d.w * ROWS + r : 0x7FFFFFFF, part, x, sum);
     }
+    store_row(a, rq, d.z, i < USED ? d.w * ROWS + r : 0x7FFFFFFF, part, x, sum);
 }
 
 template <int D, int ROWS>
 constexpr int attn_smem() {
     constexpr int stages = kTile * (D + 4), outputs = ROWS * (D + 4) * 4;
-    return (ROWS / 4) * (D / 32) * 256 + kAttnWarps * (stages > outputs ? stages : outputs);
+    return (ROWS / 4) * (D / 32) * 256 +
+           kAttnWarps * (outputs_beside<D, ROWS>() ? stages + outputs : stages > outputs ? stages : outputs);
 }
 
 }  // namespace kv4
@@ -1126,9 +1210,10 @@ convrot_status launch_attention(AttnArgs a, int64_t ctas, int sms, cudaStream_t 
                                                       attn_smem<D, ROWS>()) != cudaSuccess)
         return CONVROT_ERR_CUDA;
     if (ctas > static_cast<int64_t>(sms) * per_sm) ctas = static_cast<int64_t>(sms) * per_sm;
-    attention_kernel<D, ROWS><<<static_cast<unsigned>(ctas), kAttnThreads, attn_smem<D, ROWS>(), stream>>>(a);
-    if (launched() != CONVROT_OK) return CONVROT_ERR_CUDA;
-    return host::launch_dependent(combine_kernel<D, ROWS>, dim3(static_cast<unsigned>(ctas)), dim3(kAttnThreads), 0,
+    const dim3 grid(static_cast<unsigned>(ctas));
+    if (host::launch_dependent(attention_kernel<D, ROWS>, grid, dim3(kAttnThreads), attn_smem<D, ROWS>(), stream, a) != CONVROT_OK)
+        return CONVROT_ERR_CUDA;
+    return host::launch_dependent(combine_kernel<D, ROWS>, grid, dim3(kCombineThreads), 0,
                                   stream, a);
 }
 
