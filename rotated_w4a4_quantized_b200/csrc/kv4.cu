@@ -395,7 +395,7 @@ struct Segment {
 };
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS == 8 ? 3 : 4) attention_kernel(AttnArgs a) {
     constexpr bool HALF = ROWS == 4;    // the columns hold the two bytes of four queries
     constexpr int NT = HALF ? 1 : ROWS / 8;
     constexpr int NS = HALF ? 2 : 4;    // scores a thread, 16-key block and column tile
@@ -451,14 +451,15 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    long long share = total < (1ll << 31)
-                          ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
-                          : (total + gridDim.x - 1) / static_cast<long long>(gridDim.x);
-    if (share < kMinUnits) share = kMinUnits;
-    const long long u0 = share * blockIdx.x;
-    const long long u1 = min(u0 + share, total);
+    // CTA c of the first `ctas` takes units [c total / ctas, (c + 1) total / ctas)
+    const long long ctas = min(static_cast<long long>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
+    auto first_of = [&](long long c) {
+        const long long n = c * total;
+        return n < (1ll << 32) ? static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(ctas)) : n / ctas;
+    };
     if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (u0 >= total) return;
+    if (blockIdx.x >= ctas) return;
+    const long long u0 = first_of(blockIdx.x), u1 = first_of(blockIdx.x + 1);
     if (mine > 0 && before <= u0 && u0 < before + mine) {
         long long at = before;
         for (int b = b_lo; b < b_hi; ++b) {
@@ -546,26 +547,33 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
                 }
                 prep::cp_async_commit();
             };
-            auto page_of = [&](const Segment &sg, int j0) {
-                int id = -1;
-                if (j0 < sg.rq.len) {
-                    id = a.table[sg.b * a.max_pages + (j0 >> a.c.page_shift)];
-                    if (id < 0 || id >= num_pages) {
-                        if (lane == 0) page_error();
-                        id = -1;
-                    }
-                }
-                return id;
-            };
-            auto request = [&](const Segment &sg, int tile) {
-                in_page = (tile * TILE) & page_mask;
-                if (one_page) ids[0] = page_of(sg, tile * TILE);
-                else
-    #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) ids[blk] = page_of(sg, tile * TILE + 16 * blk);
-                copy(sg.h, a.c.kc, a.c.ks, 0);
-            };
-            // The first of a segment's tiles, and this thread's queries of it.
+            // Table entries are read a tile ahead of their use (-1 behind the
+    // request's end), and checked when they are used.
+    int ahead[NB];
+    auto look_ahead = [&](const Segment &sg, int tile) {
+        const int *row = a.table + sg.b * a.max_pages;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+            if (blk && one_page) break;
+            const int64_t j0 = static_cast<int64_t>(tile) * TILE + 16 * blk;
+            ahead[blk] = j0 < sg.rq.len ? row[j0 >> a.c.page_shift] : -1;
+        }
+    };
+    auto request = [&](const Segment &sg, int tile) {
+        in_page = (tile * TILE) & page_mask;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+            if (blk && one_page) break;
+            ids[blk] = ahead[blk];
+            if (ids[blk] < 0 || ids[blk] >= num_pages) {
+                ids[blk] = -1;
+                if (tile * TILE + 16 * blk < sg.rq.len && lane == 0) page_error();
+            }
+        }
+        copy(sg.h, a.c.kc, a.c.ks, 0);
+        look_ahead(sg, tile + kAttnWarps);
+    };
+    // The first of a segment's tiles, and this thread's queries of it.
     uint4 raw[2];
     auto query_at = [&](const Segment &sg, int i) -> const uint16_t * {
         const int row = sg.rb * ROWS + i / LANES, qi = row / a.G;
@@ -583,6 +591,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
     auto start = [&](const Segment &sg) {
         load_query(sg, tid);
         if (sg.tile0 + warp < sg.tile1) {
+            look_ahead(sg, sg.tile0 + warp);
             request(sg, sg.tile0 + warp);
             copy(sg.h, a.c.vc, a.c.vs, 1);
         }
@@ -1034,7 +1043,7 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
             }
         }
         if (!whole && sg.u0 >= u0 && tid == 0)
-            a.desc[blockIdx.x] = make_int4(static_cast<int>((sg.u1 - 1) / share), sg.b, h, sg.rb);
+            a.desc[blockIdx.x] = make_int4(static_cast<int>((sg.u1 * ctas - 1) / total), sg.b, h, sg.rb);   // the owner of its last unit
         if constexpr (!BESIDE) {
             __syncthreads();            // the outputs have been read
             if (!last) start(next);
@@ -1045,58 +1054,67 @@ __global__ void __launch_bounds__(kAttnThreads, ROWS <= 8 && D <= 128 ? 4 : 2) a
 // CTA c joins the parts of the request that CTA c of attention_kernel began
 // and did not end: 16 channels of a row a thread, the parts dealt out to the
 // groups of ROWS D / 16 threads that the CTA has, which are joined at the end.
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 512;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
     constexpr int LANES = D / 16, USED = ROWS * LANES, WIDTH = USED < 32 ? 32 : USED, GROUPS = kCombineThreads / WIDTH;
-    static_assert(WIDTH % 32 == 0 && WIDTH <= kCombineThreads, "whole warps a group");
-    __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][4][WIDTH];
-    __shared__ float totals[GROUPS > 1 ? GROUPS - 1 : 1][WIDTH];
+    static_assert(WIDTH % 32 == 0 && WIDTH <= kCombineThreads / 2, "whole warps a group");
+    __shared__ float4 sums[GROUPS - 1][4][WIDTH];
+    __shared__ float2 tops[GROUPS][WIDTH];
     ptx::grid_dependency_wait();
     const int4 d = a.desc[blockIdx.x];
     if (d.x < 0) return;
-    const Request rq = request_of<ROWS>(a, d.y);
     const int i = threadIdx.x % WIDTH, group = threadIdx.x / WIDTH, r = min(i / LANES, ROWS - 1), part = i % LANES;
     const int c0 = blockIdx.x, count = d.x - c0 + 1;
     auto at = [&](int k) {   // the k-th part: the first is its CTA's second
         return a.parts + (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * (ROWS * (D + 2));
     };
-    float top = -INFINITY;
+    // the group's parts, relative to the largest of their references
+    float x[16] = {}, sum = 0.0f, top = -INFINITY;
+    if (group < count) {
 #pragma unroll 4
-    for (int k = 0; k < count; ++k) top = fmaxf(top, at(k)[2 * r]);
-    const float safe = top == -INFINITY ? 0.0f : top;
-    float x[16] = {}, sum = 0.0f;
-#pragma unroll 4
-    for (int k = group; k < count; k += GROUPS) {
-        const float *p = at(k);
-        const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * r);
-        const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
-        const float4 y0 = src[0], y1 = src[1], y2 = src[2], y3 = src[3];
-        const float f = ex2(ml.x - safe);
-        sum += f * ml.y;
-        const float y[16] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w, y2.x, y2.y, y2.z, y2.w, y3.x, y3.y, y3.z, y3.w};
+        for (int k = group; k < count; k += GROUPS) top = fmaxf(top, at(k)[2 * r]);
+        const float safe = top == -INFINITY ? 0.0f : top;
+#pragma unroll 2
+        for (int k = group; k < count; k += GROUPS) {
+            const float *p = at(k);
+            const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * r);
+            const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
+            const float4 y0 = src[0], y1 = src[1], y2 = src[2], y3 = src[3];
+            const float f = ex2(ml.x - safe);
+            sum += f * ml.y;
+            const float y[16] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w, y2.x, y2.y, y2.z, y2.w, y3.x, y3.y, y3.z, y3.w};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] += f * y[e];
-    }
-    if constexpr (GROUPS > 1) {
+            for (int e = 0; e < 16; ++e) x[e] += f * y[e];
+        }
         if (group) {
-            totals[group - 1][i] = sum;
 #pragma unroll
             for (int e = 0; e < 4; ++e) sums[group - 1][e][i] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
-        __syncthreads();
-        if (group) return;
-        for (int k = 0; k < GROUPS - 1; ++k) {
-            sum += totals[k][i];
+        tops[group][i] = make_float2(top, sum);
+    }
+    __syncthreads();
+    if (group) return;
+    const Request rq = request_of<ROWS>(a, d.y);
+    const int groups = min(GROUPS, count);
+    float all = top;
+    for (int k = 1; k < groups; ++k) all = fmaxf(all, tops[k][i].x);
+    const float safe = all == -INFINITY ? 0.0f : all, f0 = ex2(top - safe);
+    sum *= f0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 y = sums[k][e][i];
-                x[4 * e] += y.x;
-                x[4 * e + 1] += y.y;
-                x[4 * e + 2] += y.z;
-                x[4 * e + 3] += y.w;
-            }
+    for (int e = 0; e < 16; ++e) x[e] *= f0;
+    for (int k = 1; k < groups; ++k) {
+        const float2 t = tops[k][i];
+        const float f = ex2(t.x - safe);
+        sum += f * t.y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 y = sums[k - 1][e][i];
+            x[4 * e] += f * y.x;
+            x[4 * e + 1] += f * y.y;
+            x[4 * e + 2] += f * y.z;
+            x[4 * e + 3] += f * y.w;
         }
     }
     store_row(a, rq, d.z, i < USED ? d.w * ROWS + r : 0x7FFFFFFF, part, x, sum);
@@ -1128,14 +1146,11 @@ convrot_status setup(int *dev) {
         ok &= set_smem(attention_kernel<64, 4>, attn_smem<64, 4>());
         ok &= set_smem(attention_kernel<64, 8>, attn_smem<64, 8>());
         ok &= set_smem(attention_kernel<64, 16>, attn_smem<64, 16>());
-        ok &= set_smem(attention_kernel<64, 32>, attn_smem<64, 32>());
         ok &= set_smem(attention_kernel<128, 4>, attn_smem<128, 4>());
         ok &= set_smem(attention_kernel<128, 8>, attn_smem<128, 8>());
         ok &= set_smem(attention_kernel<128, 16>, attn_smem<128, 16>());
-        ok &= set_smem(attention_kernel<128, 32>, attn_smem<128, 32>());
         ok &= set_smem(attention_kernel<256, 4>, attn_smem<256, 4>());
         ok &= set_smem(attention_kernel<256, 8>, attn_smem<256, 8>());
-        ok &= set_smem(attention_kernel<256, 16>, attn_smem<256, 16>());
         return ok;
     });
 }
@@ -1180,11 +1195,11 @@ unsigned row_grid(int64_t threads, int sms) {
     return static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
 }
 
-// Rows of a block: the smallest of 4, 8, 16 and 32 (16 with D = 256, whose
+// Rows of a block: the smallest of 4, 8 and 16 (8 with D = 256, whose
 // accumulators fill the registers) that holds an average request's rows.
 int block_rows(int64_t T, int64_t B, int G, int D) {
     const int64_t rows = (T + B - 1) / B * G;
-    return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
+    return rows <= 4 ? 4 : rows <= 8 || D == 256 ? 8 : 16;
 }
 
 // CTAs that can have work at most, from what the host knows.
@@ -1339,12 +1354,9 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
     const int sms = host::g_dev[dev].num_sms;
     auto go = [&](auto d) {
         constexpr int DIM = decltype(d)::value;
-        switch (rows) {
-            case 4: return launch_attention<DIM, 4>(a, ctas, sms, stream);
-            case 8: return launch_attention<DIM, 8>(a, ctas, sms, stream);
-            case 16: return launch_attention<DIM, 16>(a, ctas, sms, stream);
-        }
-        return launch_attention<DIM, DIM == 256 ? 16 : 32>(a, ctas, sms, stream);
+        if (rows == 4) return launch_attention<DIM, 4>(a, ctas, sms, stream);
+        if (rows == 8) return launch_attention<DIM, 8>(a, ctas, sms, stream);
+        return launch_attention<DIM, DIM == 256 ? 8 : 16>(a, ctas, sms, stream);
     };
     return D == 64 ? go(std::integral_constant<int, 64>{})
                    : D == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 256>{});
