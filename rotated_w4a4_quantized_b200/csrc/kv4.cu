@@ -1054,7 +1054,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
 // CTA c joins the parts of the request that CTA c of attention_kernel began
 // and did not end: 16 channels of a row a thread, the parts dealt out to the
 // groups of ROWS D / 16 threads that the CTA has, which are joined at the end.
-constexpr int kCombineThreads = 512;
+constexpr int kCombineThreads = 256;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
