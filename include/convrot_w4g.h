@@ -13,10 +13,14 @@
  *      packed as in convrot.h (two codes per byte, low nibble = even channel,
  *      4-bit two's complement).  The scale is rounded before the codes are
  *      chosen, so the codes make up for its rounding.
- * Activations: xr = bf16_rne(x R) as in convrot_w4a16.h, or xr = x with
- * group = 0.  Product, in fp32:
+ * Activations: xr = x R (fp32), or x with group = 0, held as 16-bit whole
+ * numbers with one fp32 factor for every 256 channels of a row: off by at most
+ * 2^-16 of the largest of the 256.  Product:
  *      y[m][n] = bf16_rne( sum_b s[n][b] (sum_{k in b} xr[m][k] q[n][k])
- *                          + bias[n] ).
+ *                          + bias[n] ),
+ * with exact sums inside a scale group and fp32 beyond.  256 channels whose
+ * largest value is below 2^-100 count as 0; a row with a NaN or an infinity
+ * gives NaN.
  *
  * Conventions are those of convrot.h: device pointers on the current device,
  * row-major, contiguous, 16-byte aligned; the caller owns every buffer and the
@@ -43,15 +47,15 @@ convrot_status convrot_w4g_quantize_weight(const void *w_bf16, int64_t N, int64_
                                            int scale_group, uint8_t *qw, void *sg_bf16,
                                            convrot_stream_t stream);
 
-/* Bytes of workspace convrot_w4g_linear needs: the rotated activations,
- * M * K * 2 rounded up to 256, or 0 with group = 0 (and for M <= 0 or
+/* Bytes of workspace convrot_w4g_linear needs for the activations' numbers
+ * and factors, or 0 where a few short rows need none (and for M <= 0 or
  * K <= 0).  Host-only. */
-size_t convrot_w4g_workspace_size(int64_t M, int64_t K, int group);
+size_t convrot_w4g_workspace_size(int64_t M, int64_t K);
 
 /*
  * The whole layer: x_bf16 [M][K] bf16, qw [N][K/2], sg_bf16
  * [N][K/scale_group], bias_bf16 [N] bf16 or NULL (zeros), y_bf16 [M][N].
- * workspace: at least convrot_w4g_workspace_size(M, K, group) bytes, 256-byte
+ * workspace: at least convrot_w4g_workspace_size(M, K) bytes, 256-byte
  * aligned (CONVROT_ERR_WORKSPACE otherwise; may be NULL where that is 0).
  * Made for few tokens: every 16 tokens read the weights once.  Any M is
  * accepted.

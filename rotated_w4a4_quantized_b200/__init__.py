@@ -938,7 +938,7 @@ def lib_w4g() -> ctypes.CDLL:
         P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
         _lib_w4g = _load(LIB_W4G_PATH, {
             "convrot_w4g_quantize_weight": ([P, I64, I64, I, I, P, P, P], I),
-            "convrot_w4g_workspace_size": ([I64, I64, I], SZ),
+            "convrot_w4g_workspace_size": ([I64, I64], SZ),
             "convrot_w4g_linear": ([P, P, P, P, I64, I64, I64, I, I, P, SZ, P, P], I),
         })
     return _lib_w4g
@@ -962,8 +962,8 @@ def convrot_w4g_quantize_weight(w, group: int, scale_group: int, qw=None, sg=Non
     return qw, sg
 
 
-def convrot_w4g_workspace_size(M: int, K: int, group: int) -> int:
-    return int(lib_w4g().convrot_w4g_workspace_size(M, K, group))
+def convrot_w4g_workspace_size(M: int, K: int) -> int:
+    return int(lib_w4g().convrot_w4g_workspace_size(M, K))
 
 
 def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=None, out=None,
@@ -981,7 +981,7 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
     _need_opt(bias, torch.bfloat16, "bias", (N,), x)
     L = lib_w4g()
     with _On(x):
-        need = L.convrot_w4g_workspace_size(M, K, group)
+        need = L.convrot_w4g_workspace_size(M, K)
         if workspace is not None:
             _need(workspace, torch.uint8, "workspace", None, x)
             if workspace.numel() < need:

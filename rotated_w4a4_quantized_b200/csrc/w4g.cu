@@ -9,7 +9,7 @@
 
 namespace w4g {
 
-// ------------------------------------------------------------------ weights, activations
+// ------------------------------------------------------------------ weights
 // 16 channels a thread over the matrix as one line of values: a rotation group
 // (4 or 16 threads) and a scale group (2, 4 or 8 threads) never cross a row,
 // because K is a multiple of both.
@@ -37,28 +37,85 @@ quantize_kernel(const uint16_t *__restrict__ w, int64_t threads, int group, int 
     }
 }
 
+// ------------------------------------------------------------------ activations
+// The product takes 16-bit whole numbers, n, and a factor f for every 256
+// channels of a row: x R = n f with the largest of the 256 at 32000, so the
+// rounding is at most 2^-16 of it (bf16 would be off by 2^-8 of each value).  A
+// number's high and low byte (signed) go through int8 products of their own.
+// Blocks below 2^-100 count as 0; one with a NaN or an infinity has a factor of
+// NaN.  A word's 8 channels are 16 bytes: the high bytes of the odd channels,
+// of the even ones, then the low bytes in the same order.
+constexpr int kStage = 256;                  // channels
+constexpr int kLanes = kStage / 16;          // lanes of a block, 16 channels each
+
+// The 16 channels of this lane's part of a block; whole warps call it.
+__device__ __forceinline__ void whole_numbers(float (&v)[16], int group, uint4 (&words)[2], float &factor) {
+    if (group) frag::rotate16(v, group == 256);
+    const uint32_t amax = frag::absmax_bits(v, kLanes);
+    const float top = __uint_as_float(amax);
+    const bool zero = amax < (27u << 23);
+    const float f = zero ? 0.0f : 32000.0f / top;
+    factor = zero ? 0.0f : (group ? frag::norm_of(group) : 1.0f) * (top / 32000.0f);
+    if (amax >= 0x7F800000u) factor = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int n = __float2int_rn(v[8 * half + e] * f);
+            hi[e] = static_cast<uint32_t>(n + 128) >> 8;
+            lo[e] = static_cast<uint32_t>(n);
+        }
+        auto bytes = [](uint32_t p, uint32_t q, uint32_t r, uint32_t t) {
+            return __byte_perm(__byte_perm(p, q, 0x0040), __byte_perm(r, t, 0x0040), 0x5410);
+        };
+        words[half] = make_uint4(bytes(hi[1], hi[3], hi[5], hi[7]), bytes(hi[0], hi[2], hi[4], hi[6]),
+                                 bytes(lo[1], lo[3], lo[5], lo[7]), bytes(lo[0], lo[2], lo[4], lo[6]));
+    }
+}
+
+__device__ __forceinline__ void load_part(const uint16_t *x, int64_t m, int K, int part, bool live, float (&v)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+    if (live && 16 * part < K) frag::load16(x + m * K + 16 * part, v);
+}
+
+// Numbers [block][word][row of a 16-row chunk] and factors [block][row], chunk
+// after chunk, as the product reads them.
 __global__ void __launch_bounds__(kRowThreads)
-rotate_kernel(const uint16_t *__restrict__ x, int64_t threads, int group, uint16_t *__restrict__ xr) {
+prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, uint4 *__restrict__ numbers,
+               float *__restrict__ factors) {
     // the product's CTAs may be placed as soon as there is room: they fetch
-    // weights and wait for this grid before they read xr
+    // weights and wait for this grid before they read its numbers
     ptx::launch_dependents();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < threads; i0 += step) {
-        const int64_t i = i0 + threadIdx.x;
-        float v[16] = {};
-        if (i < threads) frag::load16(x + 16 * i, v);
-        frag::rotate16(v, group == 256);
-        if (i < threads) frag::store16(xr + 16 * i, v, frag::norm_of(group));
+    const int blocks = (K + kStage - 1) / kStage, lanes = blocks * kLanes;
+    const int64_t total = M * lanes, step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < total; i0 += step) {
+        const int64_t i = i0 + threadIdx.x, m = i / lanes;
+        const int part = static_cast<int>(i % lanes);
+        float v[16], factor;
+        uint4 words[2];
+        load_part(x, m, K, part, i < total, v);
+        whole_numbers(v, group, words, factor);
+        if (i < total) {
+            const int64_t m0 = m & ~15ll;
+            const int rows = static_cast<int>(min(16ll, static_cast<long long>(M - m0)));
+            uint4 *dst = numbers + m0 * blocks * (kStage / 8) + static_cast<int64_t>(2 * part) * rows + (m - m0);
+            dst[0] = words[0];
+            dst[rows] = words[1];
+            if (part % kLanes == 0) factors[m0 * blocks + static_cast<int64_t>(part / kLanes) * rows + (m - m0)] = factor;
+        }
     }
 }
 
 // ------------------------------------------------------------------ product
-// y^T (rows x tokens) = sum over scale groups of s (codes x tokens): the
-// codes, widened exactly to bf16, are the A operand of mma.sync m16n8k16 (16
-// weight rows, 16 channels), the tokens its 8 columns.  A group's sum is
-// taken in its own fp32 accumulator and joins the row's with one FMA by the
-// scale: codes times activations are summed without any rounding of the
-// weights.
+// y^T (rows x tokens) = sum over blocks f (sum over scale groups s (codes x
+// numbers)): the codes as int8 (16 times the code: three operations for 8 of
+// them, of which two on the integer pipe) are the A operand of mma.sync
+// m16n8k32 (16 weight rows, 32 channels), the numbers its 8 columns.  Up to 4
+// tokens fill the 8 columns with both bytes of their numbers; more take a
+// product for each byte.  A group's sum is exact in int32 and joins the row's
+// with one FMA by the scale, a block's by the factor.
 //
 // One CTA has R consecutive rows (R spreads N over the SMs) and all of K.  Its
 // warps are (tile of 16 rows, part of K): part p of kp takes the 256-code
@@ -68,38 +125,42 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t threads, int group, uint16
 // word from each of 8 rows spread over all banks.  In step j of a stage lane
 // (g, t) has word 4 j + t of rows g and g + 8: the 32 channels of a step are
 // consecutive, so scale groups of 32 and more never share an accumulator.
-// Which channel sits where in the product is free as long as the activations
-// agree: they lie in shared memory as 16-byte groups of 8 channels in the
-// order (0, 4), (1, 5), (2, 6), (3, 7) of the widened words.
+//
+// With few tokens every CTA turns the rows into numbers itself while its first
+// weights are on their way; with more, prepare_kernel does it once.
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStage = 256;                  // codes
 constexpr int kStageBytes = 16 * kStage / 2;
 constexpr int kDepth = 4;
 constexpr int kRing = kWarps * kDepth * kStageBytes;
-constexpr int kActBytes = 96 * 1024;         // activations held at a time
+constexpr int kActBytes = 90 * 1024;         // numbers held at a time
 constexpr int kMaxRows = 128;                // of a CTA
+constexpr int kFusedLanes = 2 * kThreads;    // lanes of 16 channels that a CTA turns into numbers itself
 
 struct Args {
-    const uint16_t *x;       // [M][K], rotated
+    const uint16_t *x;       // [M][K], or NULL: prepared
+    const uint4 *numbers;
+    const float *factors;
     const uint8_t *qw;
     const uint16_t *sg;
     const uint16_t *bias;
     uint16_t *y;
     int64_t M, N;
-    int K, R;
-    int slice;               // stages of activations in shared memory at a time
-    int wait;                // a rotation kernel comes before this one
+    int K, R, group;
+    int slice;               // stages of numbers in shared memory at a time
 };
 
-// NT: token columns / 8.  SG: scale group.
-template <int NT, int SG>
+// TOK: tokens of a CTA, 4, 8 or 16.  SG: scale group.
+template <int TOK, int SG>
 __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
+    constexpr bool HALF = TOK == 4;          // columns 0-3 high bytes, 4-7 low bytes
+    constexpr int NT = HALF ? 1 : TOK / 8;
     constexpr int GROUPS = kStage / SG;      // scale groups of a stage
+    constexpr int STEPS = SG / 32;           // of a group
     extern __shared__ uint4 smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(8 * NT), a.M - m0));
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(16), a.M - m0));
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * a.R;
     const int rows = static_cast<int>(min(static_cast<int64_t>(a.R), a.N - n0));
     const int stages = (a.K + kStage - 1) / kStage;
@@ -112,6 +173,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * (kDepth * kStageBytes);
     uint4 *act = smem + kRing / 16;          // [slice * 32 words][tokens]
+    float *fac = reinterpret_cast<float *>(act + a.slice * (kStage / 8) * tokens);   // [slice][tokens]
     const uint8_t *wrow = a.qw + (n0 + 16 * tile) * (a.K / 2);
 
     auto request = [&](int stage, int slot) {
@@ -122,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
                 const int byte = stage * (kStage / 2) + 16 * c;
                 const bool live = r < tile_rows && byte < a.K / 2;
                 frag::cp_async16_or_zero(ring + slot * kStageBytes + r * 128 + ((c ^ (r & 7)) << 4),
-                                   live ? wrow + static_cast<int64_t>(r) * (a.K / 2) + byte : a.qw, live);
+                                         live ? wrow + static_cast<int64_t>(r) * (a.K / 2) + byte : a.qw, live);
             }
         }
         prep::cp_async_commit();
@@ -143,21 +205,37 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     for (int i = 0; i < kDepth - 1; ++i) request(part + i * parts, i);
     uint16_t next[2][GROUPS];
     load_scales(part, next);
-    if (a.wait) ptx::grid_dependency_wait();
 
+    const frag::CodeMasks masks;
+    // this lane's column of the numbers: a token's (both bytes', or with HALF
+    // one byte's) 8 or 16 bytes of a word
+    const int token = HALF ? g & 3 : g;
     float acc[NT][4] = {};
     int stage = part, slot = 0;
+    if (!a.x) ptx::grid_dependency_wait();
     for (int s0 = 0; s0 < stages; s0 += a.slice) {
         const int s1 = min(stages, s0 + a.slice);
         if (s0) __syncthreads();             // the last slice has been read
-        const int words = (s1 - s0) * (kStage / 8);
-        for (int i = tid; i < words * tokens; i += kThreads) {
-            const int m = i / words, w = i % words;
-            const int k = (s0 * (kStage / 8) + w) * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k < a.K) v = *reinterpret_cast<const uint4 *>(a.x + (m0 + m) * a.K + k);
-            act[w * tokens + m] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                             __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        if (a.x) {                           // one slice
+            const int lanes = stages * kLanes;
+            for (int i0 = 0; i0 < tokens * lanes; i0 += kThreads) {
+                const int i = i0 + tid, m = i / lanes, p = i % lanes;
+                float v[16], factor;
+                uint4 words[2];
+                load_part(a.x, m0 + m, a.K, p, m < tokens, v);
+                whole_numbers(v, a.group, words, factor);
+                if (m < tokens) {
+                    act[2 * p * tokens + m] = words[0];
+                    act[(2 * p + 1) * tokens + m] = words[1];
+                    if (p % kLanes == 0) fac[p / kLanes * tokens + m] = factor;
+                }
+            }
+        } else {
+            const int n = (s1 - s0) * (kStage / 8) * tokens;
+            const uint4 *src = a.numbers + m0 * stages * (kStage / 8) + static_cast<int64_t>(s0) * (kStage / 8) * tokens;
+            for (int i = tid; i < n; i += kThreads) act[i] = src[i];
+            const float *fsrc = a.factors + m0 * stages + static_cast<int64_t>(s0) * tokens;
+            for (int i = tid; i < (s1 - s0) * tokens; i += kThreads) fac[i] = fsrc[i];
         }
         __syncthreads();
         if (!works) continue;
@@ -173,50 +251,72 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
             frag::cp_async_wait<kDepth - 1>();
             __syncwarp();
             const uint8_t *src = reinterpret_cast<const uint8_t *>(smem) + warp * (kDepth * kStageBytes) + slot * kStageBytes + 128 * g + 4 * t4;
-            const uint4 *xs = act + ((stage - s0) * (kStage / 8) + t4) * tokens + g;
-            float part_acc[NT][4] = {};
+            const uint4 *xs = act + ((stage - s0) * (kStage / 8) + t4) * tokens + token;
+            float block[NT][4] = {};
+            int high[NT][4], low[NT][4];
 #pragma unroll
             for (int j = 0; j < kStage / 32; ++j) {
-                uint32_t wa[4], wb[4];
-                frag::widen_bf16(*reinterpret_cast<const uint32_t *>(src + ((j ^ g) << 4)), wa);
-                frag::widen_bf16(*reinterpret_cast<const uint32_t *>(src + 1024 + ((j ^ g) << 4)), wb);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (8 * nt + g < tokens) x = xs[4 * j * tokens + 8 * nt];
-                    frag::mma_bf16(part_acc[nt], wa[0], wb[0], wa[1], wb[1], x.x, x.y);
-                    frag::mma_bf16(part_acc[nt], wa[2], wb[2], wa[3], wb[3], x.z, x.w);
-                }
-                if ((j + 1) % (SG / 32) == 0) {
-                    const int i = j / (SG / 32);
-                    const float fa = frag::bf16_f32(sc[0][i]), fb = frag::bf16_f32(sc[1][i]);
+                uint32_t ao, ae, bo, be;
+                frag::codes_s8(masks, *reinterpret_cast<const uint32_t *>(src + ((j ^ g) << 4)), ao, ae);
+                frag::codes_s8(masks, *reinterpret_cast<const uint32_t *>(src + 1024 + ((j ^ g) << 4)), bo, be);
+                const bool begins = j % STEPS == 0;
+                if constexpr (HALF) {
+                    uint2 x = make_uint2(0, 0);
+                    if (token < tokens) x = reinterpret_cast<const uint2 *>(xs + 4 * j * tokens)[g >> 2];
+                    if (begins) frag::mma_s8_first(high[0], ao, bo, ae, be, x.x, x.y);
+                    else frag::mma_s8(high[0], ao, bo, ae, be, x.x, x.y);
+                } else {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        acc[nt][0] = fmaf(fa, part_acc[nt][0], acc[nt][0]);
-                        acc[nt][1] = fmaf(fa, part_acc[nt][1], acc[nt][1]);
-                        acc[nt][2] = fmaf(fb, part_acc[nt][2], acc[nt][2]);
-                        acc[nt][3] = fmaf(fb, part_acc[nt][3], acc[nt][3]);
-                        part_acc[nt][0] = part_acc[nt][1] = part_acc[nt][2] = part_acc[nt][3] = 0.0f;
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (8 * nt + token < tokens) x = xs[4 * j * tokens + 8 * nt];
+                        if (begins) {
+                            frag::mma_s8_first(high[nt], ao, bo, ae, be, x.x, x.y);
+                            frag::mma_s8_first(low[nt], ao, bo, ae, be, x.z, x.w);
+                        } else {
+                            frag::mma_s8(high[nt], ao, bo, ae, be, x.x, x.y);
+                            frag::mma_s8(low[nt], ao, bo, ae, be, x.z, x.w);
+                        }
                     }
                 }
+                if ((j + 1) % STEPS == 0) {
+                    const float fa = frag::bf16_f32(sc[0][j / STEPS]), fb = frag::bf16_f32(sc[1][j / STEPS]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            block[nt][x] = fmaf(x < 2 ? fa : fb, static_cast<float>(HALF ? high[nt][x] : 256 * high[nt][x] + low[nt][x]), block[nt][x]);
+                }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int m = 8 * nt + (HALF ? 2 * (t4 & 1) : 2 * t4) + x;
+                    const float f = m < tokens ? fac[(stage - s0) * tokens + m] : 0.0f;
+                    acc[nt][x] = fmaf(f, block[nt][x], acc[nt][x]);
+                    acc[nt][2 + x] = fmaf(f, block[nt][2 + x], acc[nt][2 + x]);
+                }
             __syncwarp();                    // the slot is free again
             slot = (slot + 1) % kDepth;
         }
     }
     frag::cp_async_wait<0>();
 
-    // ---- join the parts of K in their order, add the bias, round
+    // ---- join the bytes and the parts of K in their order, add the bias, round
     __syncthreads();
     float *red = reinterpret_cast<float *>(smem);   // [parts][tokens][tiles * 16]
     const int pitch = tiles * 16;
+    if constexpr (HALF)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[0][x] = fmaf(256.0f, acc[0][x], __shfl_xor_sync(0xFFFFFFFFu, acc[0][x], 2));
     if (works) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int m = 8 * nt + 2 * t4 + (x & 1);
-                if (m < tokens) red[(part * tokens + m) * pitch + 16 * tile + g + 8 * (x >> 1)] = acc[nt][x];
+                if (m < (HALF ? min(4, tokens) : tokens)) red[(part * tokens + m) * pitch + 16 * tile + g + 8 * (x >> 1)] = acc[nt][x] * (1.0f / 16.0f);
             }
     }
     __syncthreads();
@@ -237,16 +337,17 @@ namespace {
 
 using namespace w4g;
 
-template <int NT, int SG>
+constexpr int kMostSmem = kRing + kActBytes + 4096;
+
+template <int TOK, int SG>
 bool opt_in() {
-    return cudaFuncSetAttribute(product_kernel<NT, SG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kRing + kActBytes) == cudaSuccess;
+    return cudaFuncSetAttribute(product_kernel<TOK, SG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) == cudaSuccess;
 }
 
 convrot_status setup(int *dev) {
     return host::device_setup(dev, [] {
-        return opt_in<1, 32>() && opt_in<1, 64>() && opt_in<1, 128>() && opt_in<2, 32>() && opt_in<2, 64>() &&
-               opt_in<2, 128>();
+        return opt_in<4, 32>() && opt_in<4, 64>() && opt_in<4, 128>() && opt_in<8, 32>() && opt_in<8, 64>() &&
+               opt_in<8, 128>() && opt_in<16, 32>() && opt_in<16, 64>() && opt_in<16, 128>();
     });
 }
 
@@ -264,20 +365,21 @@ unsigned row_grid(int64_t threads, int sms) {
     return static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
 }
 
-template <int NT>
-convrot_status launch_product(const Args &a, int scale_group, int sms, cudaStream_t stream) {
-    const int stages = (a.K + kStage - 1) / kStage;
-    const int slice = a.slice < stages ? a.slice : stages;
-    const int64_t tokens = a.M < 8 * NT ? a.M : 8 * NT;
-    const dim3 grid(static_cast<unsigned>((a.N + a.R - 1) / a.R), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)));
-    const size_t smem = kRing + static_cast<size_t>(slice) * kStage * 2 * tokens;
+// Whether every CTA of the product turns the rows into numbers itself.
+bool fused(int64_t M, int64_t K) { return M <= 16 && M * ((K + kStage - 1) / kStage) * kLanes <= kFusedLanes; }
+
+template <int TOK>
+convrot_status launch_product(const Args &a, int scale_group, cudaStream_t stream) {
+    const int64_t tokens = a.M < 16 ? a.M : 16;
+    const dim3 grid(static_cast<unsigned>((a.N + a.R - 1) / a.R), static_cast<unsigned>((a.M + 15) / 16));
+    const size_t smem = kRing + a.slice * (kStage * 2 + sizeof(float)) * tokens;
     auto go = [&](auto *kernel) {
-        if (a.wait) return host::launch_dependent(kernel, grid, dim3(kThreads), smem, stream, a);
+        if (!a.x) return host::launch_dependent(kernel, grid, dim3(kThreads), smem, stream, a);
         kernel<<<grid, kThreads, smem, stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
     };
-    return scale_group == 32 ? go(product_kernel<NT, 32>)
-                             : scale_group == 64 ? go(product_kernel<NT, 64>) : go(product_kernel<NT, 128>);
+    return scale_group == 32 ? go(product_kernel<TOK, 32>)
+                             : scale_group == 64 ? go(product_kernel<TOK, 64>) : go(product_kernel<TOK, 128>);
 }
 
 }  // namespace
@@ -301,9 +403,10 @@ convrot_status convrot_w4g_quantize_weight(const void *w_bf16, int64_t N, int64_
     return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
-size_t convrot_w4g_workspace_size(int64_t M, int64_t K, int group) {
-    if (M <= 0 || K <= 0 || group == 0) return 0;
-    return host::round256(static_cast<size_t>(M) * static_cast<size_t>(K) * 2);
+size_t convrot_w4g_workspace_size(int64_t M, int64_t K) {
+    if (M <= 0 || K <= 0 || K > CONVROT_MAX_K || fused(M, K)) return 0;
+    const size_t blocks = static_cast<size_t>(M) * static_cast<size_t>((K + kStage - 1) / kStage);
+    return host::round256(blocks * kStage * 2) + host::round256(blocks * sizeof(float));
 }
 
 convrot_status convrot_w4g_linear(const void *x_bf16, const uint8_t *qw, const void *sg_bf16,
@@ -312,9 +415,9 @@ convrot_status convrot_w4g_linear(const void *x_bf16, const uint8_t *qw, const v
                                   void *y_bf16, convrot_stream_t stream) {
     convrot_status st = check_shape(M, K, group, scale_group);
     if (st != CONVROT_OK) return st;
-    if (N < 0 || N > (int64_t(1) << 30) || M > 65535 * 8 || M * N > (int64_t(1) << 40)) return CONVROT_ERR_SHAPE;
+    if (N < 0 || N > (int64_t(1) << 30) || M > 65535 * 16 || M * N > (int64_t(1) << 40)) return CONVROT_ERR_SHAPE;
     if (M == 0 || N == 0) return CONVROT_OK;
-    const size_t need = convrot_w4g_workspace_size(M, K, group);
+    const size_t need = convrot_w4g_workspace_size(M, K);
     if (!x_bf16 || !qw || !sg_bf16 || !y_bf16 || (need && !workspace)) return CONVROT_ERR_NULL;
     if (need && (ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return CONVROT_ERR_WORKSPACE;
     if (!host::aligned16({x_bf16, qw, sg_bf16, bias_bf16, y_bf16})) return CONVROT_ERR_ALIGN;
@@ -324,20 +427,25 @@ convrot_status convrot_w4g_linear(const void *x_bf16, const uint8_t *qw, const v
         return st;
     const int sms = host::g_dev[dev].num_sms;
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
-    if (group) {
-        const int64_t threads = M * (K / 16);
-        rotate_kernel<<<row_grid(threads, sms), kRowThreads, 0, stream>>>(x, threads, group, static_cast<uint16_t *>(workspace));
+    const int64_t blocks = (K + kStage - 1) / kStage, tokens = M < 16 ? M : 16;
+    uint4 *numbers = nullptr;
+    float *factors = nullptr;
+    if (need) {
+        numbers = static_cast<uint4 *>(workspace);
+        factors = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(M * blocks * kStage * 2));
+        prepare_kernel<<<row_grid(M * blocks * kLanes, sms), kRowThreads, 0, stream>>>(x, M, static_cast<int>(K), group, numbers, factors);
         if (cudaGetLastError() != cudaSuccess) return CONVROT_ERR_CUDA;
-        x = static_cast<const uint16_t *>(workspace);
     }
     // rows of a CTA: N spread evenly over whole waves of one CTA an SM
     const int64_t waves = (N + static_cast<int64_t>(sms) * kMaxRows - 1) / (static_cast<int64_t>(sms) * kMaxRows);
     const int R = static_cast<int>((N + sms * waves - 1) / (sms * waves));
-    const int64_t tokens = M <= 8 ? M : M < 16 ? M : 16;
-    Args a{x, qw, static_cast<const uint16_t *>(sg_bf16), static_cast<const uint16_t *>(bias_bf16),
-           static_cast<uint16_t *>(y_bf16), M, N, static_cast<int>(K), R,
-           static_cast<int>(kActBytes / (kStage * 2 * tokens)), group != 0};
-    return M <= 8 ? launch_product<1>(a, scale_group, sms, stream) : launch_product<2>(a, scale_group, sms, stream);
+    int64_t slice = kActBytes / (kStage * 2 * tokens);
+    if (slice > blocks) slice = blocks;
+    Args a{need ? nullptr : x, numbers, factors, qw, static_cast<const uint16_t *>(sg_bf16),
+           static_cast<const uint16_t *>(bias_bf16), static_cast<uint16_t *>(y_bf16), M, N, static_cast<int>(K), R, group,
+           static_cast<int>(slice)};
+    return M <= 4 ? launch_product<4>(a, scale_group, stream)
+                  : M <= 8 ? launch_product<8>(a, scale_group, stream) : launch_product<16>(a, scale_group, stream);
 }
 
 }  // extern "C"

@@ -67,13 +67,17 @@ def test_w4g_host_refusals():
     assert q(A, 4, 1024, 64, 64, B, None, None) == 1
     assert q(A, 4, 1024, 64, 64, B, U, None) == 4
     f = L.convrot_w4g_linear
-    ws = cr.convrot_w4g_workspace_size(4, 1024, 64)
-    assert ws == 4 * 1024 * 2 and cr.convrot_w4g_workspace_size(4, 1024, 0) == 0
-    assert cr.convrot_w4g_workspace_size(0, 1024, 64) == 0
-    assert f(A, B, B, None, 4, 8, 1024, 64, 64, A, ws - 1, B, None) == 5
-    assert f(A, B, B, None, 4, 8, 1024, 64, 64, U, ws, B, None) == 5
-    assert f(A, B, B, None, 4, 8, 1024, 64, 64, None, 0, B, None) == 1
-    assert f(A, B, B, None, 4, 8, 1024, 32, 64, A, ws, B, None) == 2
+    # a few short rows need no workspace; beyond, two bytes a channel of whole
+    # 256-channel blocks and a factor for each
+    assert cr.convrot_w4g_workspace_size(1, 16384) == 0 and cr.convrot_w4g_workspace_size(16, 1024) == 0
+    assert cr.convrot_w4g_workspace_size(0, 1024) == 0
+    assert cr.convrot_w4g_workspace_size(17, 1024) == 17 * 4 * 512 + 512
+    assert cr.convrot_w4g_workspace_size(2, 16384 + 64) == 2 * 65 * 512 + 768
+    ws = cr.convrot_w4g_workspace_size(40, 1024)
+    assert f(A, B, B, None, 40, 8, 1024, 64, 64, A, ws - 1, B, None) == 5
+    assert f(A, B, B, None, 40, 8, 1024, 64, 64, U, ws, B, None) == 5
+    assert f(A, B, B, None, 40, 8, 1024, 64, 64, None, 0, B, None) == 1
+    assert f(A, B, B, None, 40, 8, 1024, 32, 64, A, ws, B, None) == 2
     assert f(A, B, B, None, 4, BIG, 1024, 64, 64, A, ws, B, None) == 3
     assert f(A, B, B, None, 1 << 22, 8, 1024, 0, 64, None, 0, B, None) == 3
     assert f(A, B, B, None, -1, 8, 1024, 0, 64, None, 0, B, None) == 3
