@@ -80,10 +80,15 @@ __device__ __forceinline__ void load_part(const uint16_t *x, int64_t m, int K, i
     if (live && 16 * part < K) frag::load16(x + m * K + 16 * part, v);
 }
 
-// Numbers [block][word][row of a 16-row chunk] and factors [block][row], chunk
-// after chunk, as the product reads them.
+// Where a row's 16 bytes of a word lie among the `pitch` places of the word:
+// with 8 or 16 places the rows of neighbouring words are turned against each
+// other, so that the 8 lanes of a 128-byte read hit all banks.
+__device__ __forceinline__ int place(int word, int row, int pitch) { return pitch >= 8 ? row ^ ((word & 3) << 1) : row; }
+
+// Numbers [block][word][pitch] and factors [block][pitch] of every 16 rows, as
+// the product holds them.
 __global__ void __launch_bounds__(kRowThreads)
-prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, uint4 *__restrict__ numbers,
+prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, int pitch, uint4 *__restrict__ numbers,
                float *__restrict__ factors) {
     // the product's CTAs may be placed as soon as there is room: they fetch
     // weights and wait for this grid before they read its numbers
@@ -98,12 +103,12 @@ prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, uint
         load_part(x, m, K, part, i < total, v);
         whole_numbers(v, group, words, factor);
         if (i < total) {
-            const int64_t m0 = m & ~15ll;
-            const int rows = static_cast<int>(min(16ll, static_cast<long long>(M - m0)));
-            uint4 *dst = numbers + m0 * blocks * (kStage / 8) + static_cast<int64_t>(2 * part) * rows + (m - m0);
-            dst[0] = words[0];
-            dst[rows] = words[1];
-            if (part % kLanes == 0) factors[m0 * blocks + static_cast<int64_t>(part / kLanes) * rows + (m - m0)] = factor;
+            const int64_t chunk = (m >> 4) * blocks;
+            const int r = static_cast<int>(m & 15);
+            uint4 *dst = numbers + (chunk * (kStage / 8) + 2 * part) * pitch;
+            dst[place(2 * part, r, pitch)] = words[0];
+            dst[pitch + place(2 * part + 1, r, pitch)] = words[1];
+            if (part % kLanes == 0) factors[(chunk + part / kLanes) * pitch + r] = factor;
         }
     }
 }
@@ -120,8 +125,7 @@ prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, uint
 // One CTA has R consecutive rows (R spreads N over the SMs) and all of K.  Its
 // warps are (tile of 16 rows, part of K): part p of kp takes the 256-code
 // stages p, p + kp, ..., each copied to the warp's own ring in shared memory
-// with cp.async (four stages of 16 rows x 128 bytes; no barrier between
-// warps).  16-byte chunk c of row r lies at c ^ (r mod 8), so the reads of one
+// with cp.async (16 rows x 128 bytes a stage; no barrier between warps).  16-byte chunk c of row r lies at c ^ (r mod 8), so the reads of one
 // word from each of 8 rows spread over all banks.  In step j of a stage lane
 // (g, t) has word 4 j + t of rows g and g + 8: the 32 channels of a step are
 // consecutive, so scale groups of 32 and more never share an accumulator.
@@ -131,9 +135,12 @@ prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, uint
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStageBytes = 16 * kStage / 2;
-constexpr int kDepth = 4;
-constexpr int kRing = kWarps * kDepth * kStageBytes;
-constexpr int kActBytes = 90 * 1024;         // numbers held at a time
+// Stages of a warp's ring: with few tokens the weights' latency counts, with
+// more the room for their numbers.
+__host__ __device__ constexpr int depth_of(int tok) { return tok == 4 ? 4 : 3; }
+__host__ __device__ constexpr int ring_bytes(int tok) { return kWarps * depth_of(tok) * kStageBytes; }
+// numbers and factors held at a time
+__host__ __device__ constexpr int act_bytes(int tok) { return 224 * 1024 - ring_bytes(tok); }
 constexpr int kMaxRows = 128;                // of a CTA
 constexpr int kFusedLanes = 2 * kThreads;    // lanes of 16 channels that a CTA turns into numbers itself
 
@@ -157,13 +164,28 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     constexpr int NT = HALF ? 1 : TOK / 8;
     constexpr int GROUPS = kStage / SG;      // scale groups of a stage
     constexpr int STEPS = SG / 32;           // of a group
+    constexpr int kDepth = depth_of(TOK);
     extern __shared__ uint4 smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(16), a.M - m0));
+    const int pitch = HALF ? tokens : TOK;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * a.R;
     const int rows = static_cast<int>(min(static_cast<int64_t>(a.R), a.N - n0));
-    const int stages = (a.K + kStage - 1) / kStage;
+    const int stages = (a.K + kStage - 1) / kStage, lanes = stages * kLanes;
+
+    // rows that the CTA turns into numbers itself: their first values first
+    uint4 raw[2];
+    auto load_raw = [&](int i) {
+        const int m = i / lanes, p = i % lanes;
+        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+        if (m < tokens && 16 * p < a.K) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.x + m * a.K + 16 * p);
+            raw[0] = src[0];
+            raw[1] = src[1];
+        }
+    };
+    if (a.x) load_raw(tid);
     const int tiles = (rows + 15) / 16;
     const int parts = min(kWarps / tiles, stages);
     const int tile = warp % tiles, part = warp / tiles;
@@ -172,19 +194,22 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     const int groups = a.K / SG;
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * (kDepth * kStageBytes);
-    uint4 *act = smem + kRing / 16;          // [slice * 32 words][tokens]
-    float *fac = reinterpret_cast<float *>(act + a.slice * (kStage / 8) * tokens);   // [slice][tokens]
-    const uint8_t *wrow = a.qw + (n0 + 16 * tile) * (a.K / 2);
+    uint4 *act = smem + ring_bytes(TOK) / 16;   // [slice * 32 words][pitch]
+    float *fac = reinterpret_cast<float *>(act + a.slice * (kStage / 8) * pitch);   // [slice][pitch]
+    // this lane's copies of a stage: rows lane / 8 + 0, 4, 8, 12, chunk lane % 8
+    const int chunk = lane & 7, copy_row = lane >> 3;
+    const uint8_t *wsrc = a.qw + (n0 + 16 * tile + copy_row) * (a.K / 2) + 16 * chunk;
 
     auto request = [&](int stage, int slot) {
         if (works && stage < stages) {
+            const bool inside = stage * (kStage / 2) + 16 * chunk < a.K / 2;
+            const uint8_t *src = wsrc + stage * (kStage / 2);
+            const uint32_t dst = ring + slot * kStageBytes + copy_row * 128;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = (lane >> 3) + 4 * i, c = lane & 7;
-                const int byte = stage * (kStage / 2) + 16 * c;
-                const bool live = r < tile_rows && byte < a.K / 2;
-                frag::cp_async16_or_zero(ring + slot * kStageBytes + r * 128 + ((c ^ (r & 7)) << 4),
-                                         live ? wrow + static_cast<int64_t>(r) * (a.K / 2) + byte : a.qw, live);
+                const bool live = inside && copy_row + 4 * i < tile_rows;
+                frag::cp_async16_or_zero(dst + i * 512 + ((chunk ^ ((copy_row + 4 * i) & 7)) << 4),
+                                         live ? src + static_cast<int64_t>(i) * (2 * a.K) : a.qw, live);
             }
         }
         prep::cp_async_commit();
@@ -201,6 +226,13 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
             }
     };
 
+    // the CTA's scales are one run of bytes: into L2 ahead of their loads, which
+    // are a stage ahead of their use
+    {
+        const uint8_t *first = reinterpret_cast<const uint8_t *>(a.sg + n0 * groups);
+        for (int64_t at = static_cast<int64_t>(tid) * 128; at < static_cast<int64_t>(rows) * groups * 2; at += kThreads * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(first + at));
+    }
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) request(part + i * parts, i);
     uint16_t next[2][GROUPS];
@@ -217,25 +249,30 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
         const int s1 = min(stages, s0 + a.slice);
         if (s0) __syncthreads();             // the last slice has been read
         if (a.x) {                           // one slice
-            const int lanes = stages * kLanes;
+#pragma unroll 1
             for (int i0 = 0; i0 < tokens * lanes; i0 += kThreads) {
                 const int i = i0 + tid, m = i / lanes, p = i % lanes;
+                if (i0) load_raw(i);
                 float v[16], factor;
                 uint4 words[2];
-                load_part(a.x, m0 + m, a.K, p, m < tokens, v);
+                frag::unpack_bf16x8(raw[0], v);
+                frag::unpack_bf16x8(raw[1], v + 8);
                 whole_numbers(v, a.group, words, factor);
                 if (m < tokens) {
-                    act[2 * p * tokens + m] = words[0];
-                    act[(2 * p + 1) * tokens + m] = words[1];
-                    if (p % kLanes == 0) fac[p / kLanes * tokens + m] = factor;
+                    act[2 * p * pitch + place(2 * p, m, pitch)] = words[0];
+                    act[(2 * p + 1) * pitch + place(2 * p + 1, m, pitch)] = words[1];
+                    if (p % kLanes == 0) fac[p / kLanes * pitch + m] = factor;
                 }
             }
         } else {
-            const int n = (s1 - s0) * (kStage / 8) * tokens;
-            const uint4 *src = a.numbers + m0 * stages * (kStage / 8) + static_cast<int64_t>(s0) * (kStage / 8) * tokens;
-            for (int i = tid; i < n; i += kThreads) act[i] = src[i];
-            const float *fsrc = a.factors + m0 * stages + static_cast<int64_t>(s0) * tokens;
-            for (int i = tid; i < (s1 - s0) * tokens; i += kThreads) fac[i] = fsrc[i];
+            // (in the same group of copies as the warp's latest weights)
+            const int n = (s1 - s0) * (kStage / 8) * pitch;
+            const int64_t from = (static_cast<int64_t>(blockIdx.y) * stages + s0) * pitch;
+            const uint4 *src = a.numbers + from * (kStage / 8);
+            for (int i = tid; i < n; i += kThreads) frag::cp_async16_or_zero(ptx::smem_u32(act + i), src + i, true);
+            for (int i = tid; i < (s1 - s0) * pitch; i += kThreads) fac[i] = a.factors[from + i];
+            prep::cp_async_commit();
+            frag::cp_async_wait<0>();
         }
         __syncthreads();
         if (!works) continue;
@@ -251,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
             frag::cp_async_wait<kDepth - 1>();
             __syncwarp();
             const uint8_t *src = reinterpret_cast<const uint8_t *>(smem) + warp * (kDepth * kStageBytes) + slot * kStageBytes + 128 * g + 4 * t4;
-            const uint4 *xs = act + ((stage - s0) * (kStage / 8) + t4) * tokens + token;
+            const uint4 *xs = act + ((stage - s0) * (kStage / 8) + t4) * pitch + (HALF ? token : token ^ (t4 << 1));
             float block[NT][4] = {};
             int high[NT][4], low[NT][4];
 #pragma unroll
@@ -262,14 +299,14 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
                 const bool begins = j % STEPS == 0;
                 if constexpr (HALF) {
                     uint2 x = make_uint2(0, 0);
-                    if (token < tokens) x = reinterpret_cast<const uint2 *>(xs + 4 * j * tokens)[g >> 2];
+                    if (token < tokens) x = reinterpret_cast<const uint2 *>(xs + 4 * j * pitch)[g >> 2];
                     if (begins) frag::mma_s8_first(high[0], ao, bo, ae, be, x.x, x.y);
                     else frag::mma_s8(high[0], ao, bo, ae, be, x.x, x.y);
                 } else {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint4 x = make_uint4(0, 0, 0, 0);
-                        if (8 * nt + token < tokens) x = xs[4 * j * tokens + 8 * nt];
+                        if (8 * nt + token < tokens) x = xs[4 * j * pitch + 8 * nt];
                         if (begins) {
                             frag::mma_s8_first(high[nt], ao, bo, ae, be, x.x, x.y);
                             frag::mma_s8_first(low[nt], ao, bo, ae, be, x.z, x.w);
@@ -293,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int m = 8 * nt + (HALF ? 2 * (t4 & 1) : 2 * t4) + x;
-                    const float f = m < tokens ? fac[(stage - s0) * tokens + m] : 0.0f;
+                    const float f = m < tokens ? fac[(stage - s0) * pitch + m] : 0.0f;
                     acc[nt][x] = fmaf(f, block[nt][x], acc[nt][x]);
                     acc[nt][2 + x] = fmaf(f, block[nt][2 + x], acc[nt][2 + x]);
                 }
@@ -306,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     // ---- join the bytes and the parts of K in their order, add the bias, round
     __syncthreads();
     float *red = reinterpret_cast<float *>(smem);   // [parts][tokens][tiles * 16]
-    const int pitch = tiles * 16;
+    const int columns = tiles * 16;
     if constexpr (HALF)
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[0][x] = fmaf(256.0f, acc[0][x], __shfl_xor_sync(0xFFFFFFFFu, acc[0][x], 2));
@@ -316,14 +353,14 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int m = 8 * nt + 2 * t4 + (x & 1);
-                if (m < (HALF ? min(4, tokens) : tokens)) red[(part * tokens + m) * pitch + 16 * tile + g + 8 * (x >> 1)] = acc[nt][x] * (1.0f / 16.0f);
+                if (m < (HALF ? min(4, tokens) : tokens)) red[(part * tokens + m) * columns + 16 * tile + g + 8 * (x >> 1)] = acc[nt][x] * (1.0f / 16.0f);
             }
     }
     __syncthreads();
     for (int i = tid; i < tokens * rows; i += kThreads) {
         const int m = i / rows, r = i % rows;
         float sum = 0.0f;
-        for (int p = 0; p < parts; ++p) sum += red[(p * tokens + m) * pitch + r];
+        for (int p = 0; p < parts; ++p) sum += red[(p * tokens + m) * columns + r];
         if (a.bias) sum += frag::bf16_f32(a.bias[n0 + r]);
         a.y[(m0 + m) * a.N + n0 + r] = frag::f32_bf16(sum);
     }
@@ -337,11 +374,11 @@ namespace {
 
 using namespace w4g;
 
-constexpr int kMostSmem = kRing + kActBytes + 4096;
 
 template <int TOK, int SG>
 bool opt_in() {
-    return cudaFuncSetAttribute(product_kernel<TOK, SG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) == cudaSuccess;
+    return cudaFuncSetAttribute(product_kernel<TOK, SG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ring_bytes(TOK) + act_bytes(TOK)) == cudaSuccess;
 }
 
 convrot_status setup(int *dev) {
@@ -365,14 +402,16 @@ unsigned row_grid(int64_t threads, int sms) {
     return static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
 }
 
+// Places of a word's rows (place()).
+int64_t pitch_of(int64_t M) { return M <= 4 ? M : M <= 8 ? 8 : 16; }
+
 // Whether every CTA of the product turns the rows into numbers itself.
 bool fused(int64_t M, int64_t K) { return M <= 16 && M * ((K + kStage - 1) / kStage) * kLanes <= kFusedLanes; }
 
 template <int TOK>
 convrot_status launch_product(const Args &a, int scale_group, cudaStream_t stream) {
-    const int64_t tokens = a.M < 16 ? a.M : 16;
     const dim3 grid(static_cast<unsigned>((a.N + a.R - 1) / a.R), static_cast<unsigned>((a.M + 15) / 16));
-    const size_t smem = kRing + a.slice * (kStage * 2 + sizeof(float)) * tokens;
+    const size_t smem = ring_bytes(TOK) + a.slice * (kStage * 2 + sizeof(float)) * pitch_of(a.M);
     auto go = [&](auto *kernel) {
         if (!a.x) return host::launch_dependent(kernel, grid, dim3(kThreads), smem, stream, a);
         kernel<<<grid, kThreads, smem, stream>>>(a);
@@ -405,7 +444,7 @@ convrot_status convrot_w4g_quantize_weight(const void *w_bf16, int64_t N, int64_
 
 size_t convrot_w4g_workspace_size(int64_t M, int64_t K) {
     if (M <= 0 || K <= 0 || K > CONVROT_MAX_K || fused(M, K)) return 0;
-    const size_t blocks = static_cast<size_t>(M) * static_cast<size_t>((K + kStage - 1) / kStage);
+    const size_t blocks = static_cast<size_t>((M + 15) / 16 * pitch_of(M)) * static_cast<size_t>((K + kStage - 1) / kStage);
     return host::round256(blocks * kStage * 2) + host::round256(blocks * sizeof(float));
 }
 
@@ -427,20 +466,22 @@ convrot_status convrot_w4g_linear(const void *x_bf16, const uint8_t *qw, const v
         return st;
     const int sms = host::g_dev[dev].num_sms;
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
-    const int64_t blocks = (K + kStage - 1) / kStage, tokens = M < 16 ? M : 16;
+    const int64_t blocks = (K + kStage - 1) / kStage, pitch = pitch_of(M), places = (M + 15) / 16 * pitch;
     uint4 *numbers = nullptr;
     float *factors = nullptr;
     if (need) {
         numbers = static_cast<uint4 *>(workspace);
-        factors = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(M * blocks * kStage * 2));
-        prepare_kernel<<<row_grid(M * blocks * kLanes, sms), kRowThreads, 0, stream>>>(x, M, static_cast<int>(K), group, numbers, factors);
+        factors = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(places * blocks * kStage * 2));
+        prepare_kernel<<<row_grid(M * blocks * kLanes, sms), kRowThreads, 0, stream>>>(x, M, static_cast<int>(K), group, static_cast<int>(pitch),
+                                                                                       numbers, factors);
         if (cudaGetLastError() != cudaSuccess) return CONVROT_ERR_CUDA;
     }
     // rows of a CTA: N spread evenly over whole waves of one CTA an SM
     const int64_t waves = (N + static_cast<int64_t>(sms) * kMaxRows - 1) / (static_cast<int64_t>(sms) * kMaxRows);
     const int R = static_cast<int>((N + sms * waves - 1) / (sms * waves));
-    int64_t slice = kActBytes / (kStage * 2 * tokens);
-    if (slice > blocks) slice = blocks;
+    // the numbers' slices: as few as the shared memory allows, of even length
+    const int64_t room = act_bytes(M <= 4 ? 4 : 8) / ((kStage * 2 + 4) * pitch), slices = (blocks + room - 1) / room;
+    const int64_t slice = (blocks + slices - 1) / slices;
     Args a{need ? nullptr : x, numbers, factors, qw, static_cast<const uint16_t *>(sg_bf16),
            static_cast<const uint16_t *>(bias_bf16), static_cast<uint16_t *>(y_bf16), M, N, static_cast<int>(K), R, group,
            static_cast<int>(slice)};

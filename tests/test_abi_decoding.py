@@ -68,10 +68,11 @@ def test_w4g_host_refusals():
     assert q(A, 4, 1024, 64, 64, B, U, None) == 4
     f = L.convrot_w4g_linear
     # a few short rows need no workspace; beyond, two bytes a channel of whole
-    # 256-channel blocks and a factor for each
+    # 256-channel blocks and a factor for each, rows in sixteens (eights)
     assert cr.convrot_w4g_workspace_size(1, 16384) == 0 and cr.convrot_w4g_workspace_size(16, 1024) == 0
     assert cr.convrot_w4g_workspace_size(0, 1024) == 0
-    assert cr.convrot_w4g_workspace_size(17, 1024) == 17 * 4 * 512 + 512
+    assert cr.convrot_w4g_workspace_size(17, 1024) == 32 * 4 * 512 + 512
+    assert cr.convrot_w4g_workspace_size(5, 4096) == 8 * 16 * 512 + 512
     assert cr.convrot_w4g_workspace_size(2, 16384 + 64) == 2 * 65 * 512 + 768
     ws = cr.convrot_w4g_workspace_size(40, 1024)
     assert f(A, B, B, None, 40, 8, 1024, 64, 64, A, ws - 1, B, None) == 5
