@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     constexpr int STEPS = SG / 32;           // of a group
     constexpr int kDepth = depth_of(TOK);
     extern __shared__ uint4 smem[];
+    __shared__ uint4 zeros;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(16), a.M - m0));
@@ -200,30 +201,53 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     const int chunk = lane & 7, copy_row = lane >> 3;
     const uint8_t *wsrc = a.qw + (n0 + 16 * tile + copy_row) * (a.K / 2) + 16 * chunk;
 
+    uint32_t copy_dst[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy_dst[i] = ring + (copy_row + 4 * i) * 128 + ((chunk ^ ((copy_row + 4 * i) & 7)) << 4);
     auto request = [&](int stage, int slot) {
         if (works && stage < stages) {
-            const bool inside = stage * (kStage / 2) + 16 * chunk < a.K / 2;
             const uint8_t *src = wsrc + stage * (kStage / 2);
-            const uint32_t dst = ring + slot * kStageBytes + copy_row * 128;
+            if (tile_rows == 16 && (stage + 1) * kStage <= a.K) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool live = inside && copy_row + 4 * i < tile_rows;
-                frag::cp_async16_or_zero(dst + i * 512 + ((chunk ^ ((copy_row + 4 * i) & 7)) << 4),
-                                         live ? src + static_cast<int64_t>(i) * (2 * a.K) : a.qw, live);
+                for (int i = 0; i < 4; ++i)
+                    prep::cp_async16(copy_dst[i] + slot * kStageBytes, src + static_cast<int64_t>(i) * (2 * a.K));
+            } else {
+                const bool inside = stage * (kStage / 2) + 16 * chunk < a.K / 2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool live = inside && copy_row + 4 * i < tile_rows;
+                    frag::cp_async16_or_zero(copy_dst[i] + slot * kStageBytes,
+                                             live ? src + static_cast<int64_t>(i) * (2 * a.K) : a.qw, live);
+                }
             }
         }
         prep::cp_async_commit();
     };
-    // scales of rows g and g + 8 of a stage
-    const uint16_t *srow = a.sg + (n0 + 16 * tile) * groups;
-    auto load_scales = [&](int stage, uint16_t (&s)[2][GROUPS]) {
+    // scales of rows g and g + 8 of a stage, two to a register: one load a row
+    // where every row's stages begin on the load's boundary
+    constexpr int PAIRS = GROUPS / 2;
+    const bool row_a = works && g < tile_rows, row_b = works && g + 8 < tile_rows;
+    const uint16_t *srow = a.sg + (n0 + 16 * tile + g) * groups;
+    const bool whole = a.K % kStage == 0;
+    auto load_row_scales = [&](const uint16_t *p, int left, uint32_t (&s)[PAIRS]) {
+        if (whole) {
+            if constexpr (PAIRS == 1) s[0] = *reinterpret_cast<const uint32_t *>(p);
+            else if constexpr (PAIRS == 2) *reinterpret_cast<uint2 *>(s) = *reinterpret_cast<const uint2 *>(p);
+            else *reinterpret_cast<uint4 *>(s) = *reinterpret_cast<const uint4 *>(p);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < GROUPS; ++i) {
-                const int b = stage * GROUPS + i, r = g + 8 * h;
-                s[h][i] = works && r < tile_rows && b < groups ? srow[static_cast<int64_t>(r) * groups + b] : 0;
+            for (int i = 0; i < PAIRS; ++i) {
+                const uint32_t lo = 2 * i < left ? p[2 * i] : 0u, hi = 2 * i + 1 < left ? p[2 * i + 1] : 0u;
+                s[i] = lo | hi << 16;
             }
+        }
+    };
+    auto load_scales = [&](int stage, uint32_t (&s)[2][PAIRS]) {
+        if (stage >= stages) return;
+        const uint16_t *p = srow + stage * GROUPS;
+        const int left = groups - stage * GROUPS;
+        if (row_a) load_row_scales(p, left, s[0]);
+        if (row_b) load_row_scales(p + 8 * static_cast<int64_t>(groups), left, s[1]);
     };
 
     // the CTA's scales are one run of bytes: into L2 ahead of their loads, which
@@ -235,13 +259,14 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     }
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) request(part + i * parts, i);
-    uint16_t next[2][GROUPS];
+    uint32_t next[2][PAIRS] = {};
     load_scales(part, next);
 
     const frag::CodeMasks masks;
     // this lane's column of the numbers: a token's (both bytes', or with HALF
-    // one byte's) 8 or 16 bytes of a word
+    // one byte's) 8 or 16 bytes of a word; columns without a token read zeros
     const int token = HALF ? g & 3 : g;
+    if (tid == 0) zeros = make_uint4(0, 0, 0, 0);
     float acc[NT][4] = {};
     int stage = part, slot = 0;
     if (!a.x) ptx::grid_dependency_wait();
@@ -278,9 +303,9 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
         if (!works) continue;
         for (; stage < s1; stage += parts) {
             request(stage + (kDepth - 1) * parts, (slot + kDepth - 1) % kDepth);
-            uint16_t sc[2][GROUPS];
+            uint32_t sc[2][PAIRS];
 #pragma unroll
-            for (int i = 0; i < GROUPS; ++i) {
+            for (int i = 0; i < PAIRS; ++i) {
                 sc[0][i] = next[0][i];
                 sc[1][i] = next[1][i];
             }
@@ -289,6 +314,9 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
             __syncwarp();
             const uint8_t *src = reinterpret_cast<const uint8_t *>(smem) + warp * (kDepth * kStageBytes) + slot * kStageBytes + 128 * g + 4 * t4;
             const uint4 *xs = act + ((stage - s0) * (kStage / 8) + t4) * pitch + (HALF ? token : token ^ (t4 << 1));
+            // HALF: lanes without a token read zeros
+            const uint2 *xh = reinterpret_cast<const uint2 *>(token < tokens ? xs : &zeros) + (g >> 2);
+            const int xh_step = token < tokens ? 8 * pitch : 0;
             float block[NT][4] = {};
             int high[NT][4], low[NT][4];
 #pragma unroll
@@ -298,15 +326,14 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
                 frag::codes_s8(masks, *reinterpret_cast<const uint32_t *>(src + 1024 + ((j ^ g) << 4)), bo, be);
                 const bool begins = j % STEPS == 0;
                 if constexpr (HALF) {
-                    uint2 x = make_uint2(0, 0);
-                    if (token < tokens) x = reinterpret_cast<const uint2 *>(xs + 4 * j * pitch)[g >> 2];
+                    const uint2 x = xh[j * xh_step];
                     if (begins) frag::mma_s8_first(high[0], ao, bo, ae, be, x.x, x.y);
                     else frag::mma_s8(high[0], ao, bo, ae, be, x.x, x.y);
                 } else {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint4 x = make_uint4(0, 0, 0, 0);
-                        if (8 * nt + token < tokens) x = xs[4 * j * pitch + 8 * nt];
+                        if (8 * nt + token < tokens) x = xs[4 * j * TOK + 8 * nt];
                         if (begins) {
                             frag::mma_s8_first(high[nt], ao, bo, ae, be, x.x, x.y);
                             frag::mma_s8_first(low[nt], ao, bo, ae, be, x.z, x.w);
@@ -317,7 +344,10 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
                     }
                 }
                 if ((j + 1) % STEPS == 0) {
-                    const float fa = frag::bf16_f32(sc[0][j / STEPS]), fb = frag::bf16_f32(sc[1][j / STEPS]);
+                    constexpr uint32_t upper = 0xFFFF0000u;
+                    const int i = j / STEPS;
+                    const float fa = __uint_as_float(i & 1 ? sc[0][i >> 1] & upper : sc[0][i >> 1] << 16);
+                    const float fb = __uint_as_float(i & 1 ? sc[1][i >> 1] & upper : sc[1][i >> 1] << 16);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -405,8 +435,18 @@ unsigned row_grid(int64_t threads, int sms) {
 // Places of a word's rows (place()).
 int64_t pitch_of(int64_t M) { return M <= 4 ? M : M <= 8 ? 8 : 16; }
 
-// Whether every CTA of the product turns the rows into numbers itself.
-bool fused(int64_t M, int64_t K) { return M <= 16 && M * ((K + kStage - 1) / kStage) * kLanes <= kFusedLanes; }
+// Stages of numbers that the shared memory holds beside the weights' rings.
+int64_t stages_held(int64_t M) {
+    const int tok = M <= 4 ? 4 : M <= 8 ? 8 : 16;
+    return act_bytes(tok) / ((kStage * 2 + static_cast<int64_t>(sizeof(float))) * pitch_of(M));
+}
+
+// Whether every CTA of the product turns the rows into numbers itself: few
+// enough of them, all held at once.
+bool fused(int64_t M, int64_t K) {
+    const int64_t blocks = (K + kStage - 1) / kStage;
+    return M <= 16 && M * blocks * kLanes <= kFusedLanes && blocks <= stages_held(M);
+}
 
 template <int TOK>
 convrot_status launch_product(const Args &a, int scale_group, cudaStream_t stream) {
@@ -480,7 +520,7 @@ convrot_status convrot_w4g_linear(const void *x_bf16, const uint8_t *qw, const v
     const int64_t waves = (N + static_cast<int64_t>(sms) * kMaxRows - 1) / (static_cast<int64_t>(sms) * kMaxRows);
     const int R = static_cast<int>((N + sms * waves - 1) / (sms * waves));
     // the numbers' slices: as few as the shared memory allows, of even length
-    const int64_t room = act_bytes(M <= 4 ? 4 : 8) / ((kStage * 2 + 4) * pitch), slices = (blocks + room - 1) / room;
+    const int64_t room = stages_held(M), slices = (blocks + room - 1) / room;
     const int64_t slice = (blocks + slices - 1) / slices;
     Args a{need ? nullptr : x, numbers, factors, qw, static_cast<const uint16_t *>(sg_bf16),
            static_cast<const uint16_t *>(bias_bf16), static_cast<uint16_t *>(y_bf16), M, N, static_cast<int>(K), R, group,
