@@ -900,21 +900,24 @@ def _load(path: str, sigs: dict) -> ctypes.CDLL:
     return L
 
 
-class _On:
-    """The operands' device as the current one; nothing to do where it is."""
-    __slots__ = ("index", "before")
+# The calls below are made once a layer and token, so their checks are a few
+# comparisons; only where one fails do the named checks above say which.
 
-    def __init__(self, t: torch.Tensor):
-        self.index = t.device.index
+def _dense(t, dtype, index: int) -> bool:
+    """A contiguous tensor of `dtype` on CUDA device `index`."""
+    return t.dtype is dtype and t.get_device() == index and t.is_contiguous()
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
 
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _call(index: int, f, *args) -> int:
+    """f(*args) with CUDA device `index` as the current one."""
+    before = torch.cuda.current_device()
+    if before == index:
+        return f(*args)
+    torch.cuda.set_device(index)
+    try:
+        return f(*args)
+    finally:
+        torch.cuda.set_device(before)
 
 
 def _raw_stream(index: int, stream):
@@ -951,14 +954,13 @@ def convrot_w4g_quantize_weight(w, group: int, scale_group: int, qw=None, sg=Non
     N, K = _rows(w, torch.bfloat16, "w")
     if scale_group not in (32, 64, 128):
         raise ConvRotError(2, "convrot_w4g_quantize_weight")
-    with _On(w):
-        qw = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device) if qw is None else qw
-        sg = torch.empty(N, K // scale_group, dtype=torch.bfloat16, device=w.device) if sg is None else sg
-        _need(qw, torch.uint8, "qw", (N, K // 2), w)
-        _need(sg, torch.bfloat16, "sg", (N, K // scale_group), w)
-        _check(lib_w4g().convrot_w4g_quantize_weight(
-            w.data_ptr(), N, K, group, scale_group, qw.data_ptr(), sg.data_ptr(),
-            _raw_stream(w.device.index, stream)), "convrot_w4g_quantize_weight")
+    qw = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device) if qw is None else qw
+    sg = torch.empty(N, K // scale_group, dtype=torch.bfloat16, device=w.device) if sg is None else sg
+    _need(qw, torch.uint8, "qw", (N, K // 2), w)
+    _need(sg, torch.bfloat16, "sg", (N, K // scale_group), w)
+    index = w.get_device()
+    _check(_call(index, lib_w4g().convrot_w4g_quantize_weight, w.data_ptr(), N, K, group, scale_group,
+                 qw.data_ptr(), sg.data_ptr(), _raw_stream(index, stream)), "convrot_w4g_quantize_weight")
     return qw, sg
 
 
@@ -972,32 +974,38 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
     weights of convrot_w4g_quantize_weight (the same group and scale_group).
     group 0 takes x as it is: rotated already, or with weights that are not.
     Made for few tokens: every 16 of them read the weights once."""
-    M, K = _rows(x, torch.bfloat16, "x")
     if scale_group not in (32, 64, 128):
         raise ConvRotError(2, "convrot_w4g_linear")
-    _need(qw, torch.uint8, "qw", (None, K // 2), x)
+    if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not _dense(x, torch.bfloat16, index := x.get_device())
+            or index < 0 or not _dense(qw, torch.uint8, index) or qw.dim() != 2 or 2 * qw.shape[1] != x.shape[1]
+            or not _dense(sg, torch.bfloat16, index) or sg.shape != (qw.shape[0], x.shape[1] // scale_group)
+            or (bias is not None and (not _dense(bias, torch.bfloat16, index) or bias.shape != qw.shape[:1]))):
+        _rows(x, torch.bfloat16, "x")
+        _need(qw, torch.uint8, "qw", (None, x.shape[1] // 2), x)
+        _need(sg, torch.bfloat16, "sg", (qw.shape[0], x.shape[1] // scale_group), x)
+        _need_opt(bias, torch.bfloat16, "bias", (qw.shape[0],), x)
+        raise ValueError(f"qw holds {2 * qw.shape[1]} codes a row, x {x.shape[1]} values")
+    M, K = x.shape
     N = qw.shape[0]
-    _need(sg, torch.bfloat16, "sg", (N, K // scale_group), x)
-    _need_opt(bias, torch.bfloat16, "bias", (N,), x)
     L = lib_w4g()
-    with _On(x):
-        need = L.convrot_w4g_workspace_size(M, K)
-        if workspace is not None:
-            _need(workspace, torch.uint8, "workspace", None, x)
-            if workspace.numel() < need:
-                raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} needed")
-        elif need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is None:
+        size, pw = L.convrot_w4g_workspace_size(M, K), None
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
             _keep(workspace, stream)
-        if out is None:
-            out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
-        else:
-            _need(out, torch.bfloat16, "out", (M, N), x)
-        _check(L.convrot_w4g_linear(
-            x.data_ptr(), qw.data_ptr(), sg.data_ptr(), None if bias is None else bias.data_ptr(),
-            M, N, K, group, scale_group, None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), out.data_ptr(),
-            _raw_stream(x.device.index, stream)), "convrot_w4g_linear")
+            pw = workspace.data_ptr()
+    else:
+        _need(workspace, torch.uint8, "workspace", None, x)
+        size, pw = workspace.numel(), workspace.data_ptr()
+        if size < L.convrot_w4g_workspace_size(M, K):
+            raise ValueError(f"workspace holds {size} bytes, {L.convrot_w4g_workspace_size(M, K)} needed")
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, torch.bfloat16, "out", (M, N), x)
+    _check(_call(index, L.convrot_w4g_linear, x.data_ptr(), qw.data_ptr(), sg.data_ptr(),
+                 None if bias is None else bias.data_ptr(), M, N, K, group, scale_group, pw, size,
+                 out.data_ptr(), _raw_stream(index, stream)), "convrot_w4g_linear")
     return out
 
 
@@ -1052,29 +1060,34 @@ def convrot_kv4_new_cache(num_pages: int, kv_heads: int, page: int, head_dim: in
     return Kv4Cache(codes(), scales(), codes(), scales())
 
 
-def _kv4_cache(cache, group: int) -> _Kv4CacheArg:
+def _kv4_cache(cache, group: int):
+    """(the library's struct of a cache, its device)"""
     kc, ks, vc, vs = cache
-    _need(kc, torch.uint8, "k_codes", (None, None, None, None))
+    index = kc.get_device()
     shape = kc.shape
-    _need(ks, torch.bfloat16, "k_scales", shape[:3], kc)
-    _need(vc, torch.uint8, "v_codes", shape, kc)
-    _need(vs, torch.bfloat16, "v_scales", shape[:3], kc)
+    if (index < 0 or len(shape) != 4 or not _dense(kc, torch.uint8, index) or not _dense(vc, torch.uint8, index)
+            or not _dense(ks, torch.bfloat16, index) or not _dense(vs, torch.bfloat16, index)
+            or vc.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]):
+        _need(kc, torch.uint8, "k_codes", (None, None, None, None))
+        _need(ks, torch.bfloat16, "k_scales", shape[:3], kc)
+        _need(vc, torch.uint8, "v_codes", shape, kc)
+        _need(vs, torch.bfloat16, "v_scales", shape[:3], kc)
     return _Kv4CacheArg(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1],
-                        shape[2], 2 * shape[3], group)
+                        shape[2], 2 * shape[3], group), index
 
 
-def _need_tokens(t, name: str, heads, head_dim: int, like) -> int:
+def _need_tokens(t, name: str, heads, head_dim: int, index: int) -> int:
     """bf16 [T, heads, head_dim], dense within a token; returns the values
     between tokens (columns of a fused projection's rows qualify)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
-    if (not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != head_dim
+    if (t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[2] != head_dim or t.get_device() < 0
             or (heads is not None and t.shape[1] != heads)):
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor [tokens, "
                          f"{'heads' if heads is None else heads}, {head_dim}] "
                          f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {like.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     T, H, _ = t.shape
     st, sh, sd = t.stride()
     if T == 0 or H == 0:
@@ -1111,57 +1124,60 @@ def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, pa
     (-1 new tokens: finished, its pages go back), block_table int32
     [B, max_pages] (completed in place), free_pages int32 [capacity] (a stack of
     free_count int32 [1] page ids; returned pages are pushed in place)."""
-    _need(cached, torch.int32, "cached", (None,))
-    B = cached.shape[0]
-    _need(new_tokens, torch.int32, "new_tokens", (B,), cached)
-    _need(block_table, torch.int32, "block_table", (B, None), cached)
-    _need(free_pages, torch.int32, "free_pages", (None,), cached)
-    _need(free_count, torch.int32, "free_count", (1,), cached)
+    index = cached.get_device()
+    B = cached.shape[0] if cached.dim() == 1 else -1
+    if (index < 0 or B < 0 or not _dense(cached, torch.int32, index) or not _dense(new_tokens, torch.int32, index)
+            or not _dense(block_table, torch.int32, index) or not _dense(free_pages, torch.int32, index)
+            or not _dense(free_count, torch.int32, index) or new_tokens.shape != cached.shape
+            or block_table.dim() != 2 or block_table.shape[0] != B or free_pages.dim() != 1
+            or free_count.shape != (1,)):
+        _need(cached, torch.int32, "cached", (None,))
+        _need(new_tokens, torch.int32, "new_tokens", (B,), cached)
+        _need(block_table, torch.int32, "block_table", (B, None), cached)
+        _need(free_pages, torch.int32, "free_pages", (None,), cached)
+        _need(free_count, torch.int32, "free_count", (1,), cached)
     if max_tokens < 0:
         raise ValueError("max_tokens is negative")
-    with _On(cached):
-        dev = cached.device
-        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-        result = torch.empty(4, dtype=torch.int32, device=dev)
-        _check(lib_kv4().convrot_kv4_plan(
-            cached.data_ptr(), new_tokens.data_ptr(), B, page, block_table.data_ptr(),
-            block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(),
-            max_tokens, seq_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-            result.data_ptr(), _raw_stream(dev.index, stream)), "convrot_kv4_plan")
+    dev, i32 = cached.device, torch.int32
+    seq_lens = torch.empty(B, dtype=i32, device=dev)
+    cu_q = torch.empty(B + 1, dtype=i32, device=dev)
+    slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    positions = torch.empty(max_tokens, dtype=i32, device=dev)
+    result = torch.empty(4, dtype=i32, device=dev)
+    _check(_call(index, lib_kv4().convrot_kv4_plan, cached.data_ptr(), new_tokens.data_ptr(), B, page,
+                 block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+                 free_count.data_ptr(), max_tokens, seq_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(),
+                 positions.data_ptr(), result.data_ptr(), _raw_stream(index, stream)), "convrot_kv4_plan")
     return Kv4Plan(seq_lens, cu_q, slots, positions, result)
 
 
 def convrot_kv4_append(k, v, cache, slots, group: int, stream=None) -> None:
     """Quantise keys and values, bf16 [T, kv_heads, D], into the cache at
     slots int64 [T] (negative: skipped)."""
-    c = _kv4_cache(cache, group)
-    kc = cache[0]
-    ldk = _need_tokens(k, "k", c.kv_heads, c.head_dim, kc)
-    ldv = _need_tokens(v, "v", c.kv_heads, c.head_dim, kc)
+    c, index = _kv4_cache(cache, group)
+    ldk = _need_tokens(k, "k", c.kv_heads, c.head_dim, index)
+    ldv = _need_tokens(v, "v", c.kv_heads, c.head_dim, index)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
-    _need(slots, torch.int64, "slots", (T,), kc)
-    with _On(kc):
-        _check(lib_kv4().convrot_kv4_append(c, k.data_ptr(), ldk, v.data_ptr(), ldv, slots.data_ptr(), T,
-                                            _raw_stream(kc.device.index, stream)), "convrot_kv4_append")
+    if not _dense(slots, torch.int64, index) or slots.shape != (T,):
+        _need(slots, torch.int64, "slots", (T,), cache[0])
+    _check(_call(index, lib_kv4().convrot_kv4_append, c, k.data_ptr(), ldk, v.data_ptr(), ldv, slots.data_ptr(), T,
+                 _raw_stream(index, stream)), "convrot_kv4_append")
 
 
 def convrot_kv4_read(cache, slots, group: int, k=None, v=None, stream=None):
     """The cached rows of slots int64 [T], rotated back: (k, v) bf16
     [T, kv_heads, D]; zeros where the slot is negative."""
-    c = _kv4_cache(cache, group)
+    c, index = _kv4_cache(cache, group)
     kc = cache[0]
-    _need(slots, torch.int64, "slots", (None,), kc)
+    if not _dense(slots, torch.int64, index) or slots.dim() != 1:
+        _need(slots, torch.int64, "slots", (None,), kc)
     shape = (slots.shape[0], c.kv_heads, c.head_dim)
-    with _On(kc):
-        k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if k is None else _need(k, torch.bfloat16, "k", shape, kc)
-        v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if v is None else _need(v, torch.bfloat16, "v", shape, kc)
-        _check(lib_kv4().convrot_kv4_read(c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                                          _raw_stream(kc.device.index, stream)), "convrot_kv4_read")
+    k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if k is None else _need(k, torch.bfloat16, "k", shape, kc)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if v is None else _need(v, torch.bfloat16, "v", shape, kc)
+    _check(_call(index, lib_kv4().convrot_kv4_read, c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+                 _raw_stream(index, stream)), "convrot_kv4_read")
     return k, v
 
 
@@ -1177,33 +1193,35 @@ def convrot_kv4_attention(q, cache, block_table, seq_lens, cu_q, scale: float, g
     - 1, the last of its seq_lens[b] tokens, whose rows are in the cache; its
     pages are listed in block_table[b].  Without `out`, rows behind the last
     request are whatever the new tensor held."""
-    c = _kv4_cache(cache, group)
+    c, index = _kv4_cache(cache, group)
     kc = cache[0]
-    ldq = _need_tokens(q, "q", None, c.head_dim, kc)
+    ldq = _need_tokens(q, "q", None, c.head_dim, index)
     T, heads, D = q.shape
-    _need(seq_lens, torch.int32, "seq_lens", (None,), kc)
-    B = seq_lens.shape[0]
-    _need(block_table, torch.int32, "block_table", (B, None), kc)
-    _need(cu_q, torch.int32, "cu_q", (B + 1,), kc)
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if (B < 0 or not _dense(seq_lens, torch.int32, index) or not _dense(block_table, torch.int32, index)
+            or not _dense(cu_q, torch.int32, index) or block_table.dim() != 2 or block_table.shape[0] != B
+            or cu_q.shape != (B + 1,)):
+        _need(seq_lens, torch.int32, "seq_lens", (None,), kc)
+        _need(block_table, torch.int32, "block_table", (B, None), kc)
+        _need(cu_q, torch.int32, "cu_q", (B + 1,), kc)
     L = lib_kv4()
-    with _On(kc):
-        need = L.convrot_kv4_attention_workspace_size(T, B, heads, c.kv_heads, D,
-                                                      block_table.shape[1] * c.page)
-        if workspace is None:
-            workspace = torch.empty(max(1, need), dtype=torch.uint8, device=kc.device)
-            _keep(workspace, stream)
-        else:
-            _need(workspace, torch.uint8, "workspace", None, kc)
-            if workspace.numel() < need:
-                raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} needed")
-        if out is None:
-            out = torch.empty(T, heads, D, dtype=torch.bfloat16, device=kc.device)
-        else:
-            _need(out, torch.bfloat16, "out", (T, heads, D), kc)
-        _check(L.convrot_kv4_attention(
-            c, q.data_ptr(), ldq, T, heads, block_table.data_ptr(), block_table.shape[1],
-            seq_lens.data_ptr(), cu_q.data_ptr(), B, scale, workspace.data_ptr(), workspace.numel(),
-            out.data_ptr(), _raw_stream(kc.device.index, stream)), "convrot_kv4_attention")
+    most = block_table.shape[1]
+    size = L.convrot_kv4_attention_workspace_size(T, B, heads, c.kv_heads, D, most * c.page)
+    if workspace is None:
+        workspace = torch.empty(max(1, size), dtype=torch.uint8, device=kc.device)
+        _keep(workspace, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace", None, kc)
+        if workspace.numel() < size:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, {size} needed")
+        size = workspace.numel()
+    if out is None:
+        out = torch.empty(T, heads, D, dtype=torch.bfloat16, device=kc.device)
+    else:
+        _need(out, torch.bfloat16, "out", (T, heads, D), kc)
+    _check(_call(index, L.convrot_kv4_attention, c, q.data_ptr(), ldq, T, heads, block_table.data_ptr(), most,
+                 seq_lens.data_ptr(), cu_q.data_ptr(), B, scale, workspace.data_ptr(), size, out.data_ptr(),
+                 _raw_stream(index, stream)), "convrot_kv4_attention")
     return out
 
 

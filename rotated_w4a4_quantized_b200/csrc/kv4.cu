@@ -24,8 +24,8 @@ struct Cache {
 
 // ------------------------------------------------------------------ plan
 // One pass of integer prefix sums over the requests, done by every CTA for
-// itself (B is at most 8192: three loads a thread and a block scan, a few
-// microseconds less than a second launch would cost), then a grid-stride loop
+// itself (B is at most 8192: a few loads a thread and block scans, less than a
+// second launch would cost), then a grid-stride loop
 // over the new tokens and the taken pages, each found by binary search in the
 // prefix sums in shared memory.  Nothing that one CTA writes is read by
 // another: pages that come back and go out again in the same step are read
@@ -59,10 +59,11 @@ __device__ __forceinline__ int find(const int *cu, int B, int i) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     extern __shared__ int sm[];
-    int *cu_q = sm, *cu_take = sm + (a.B + 1), *cu_back = sm + 2 * (a.B + 1);
+    int *cu_q = sm, *cu_take = cu_q + (a.B + 1), *cu_back = cu_take + (a.B + 1), *held_by = cu_back + (a.B + 1);
     __shared__ long long warp_sum[3][32];
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t count = *a.free_count;
     if (tid == 0) bad = 0;
     __syncthreads();
 
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         long long v[3] = {0, 0, 0};
         if (b < a.B) {
             const int64_t c = a.cached[b], n = a.fresh[b];
+            held_by[b] = static_cast<int>(c);
             const int64_t have = (c + mask) >> a.page_shift;
             int why = 0;
             if (c < 0 || have > a.max_pages) why = 4;
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             }
             if (why) atomicMax(&bad, why);
         }
-        // inclusive scan over the block
+        // inclusive scan over the block: lanes, then the warps' sums
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             for (int s = 1; s < 32; s <<= 1) {
@@ -97,14 +99,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             if (lane == 31) warp_sum[k][warp] = v[k];
         }
         __syncthreads();
+        if (warp < 3) {
+            long long w = warp_sum[warp][lane];
+            for (int s = 1; s < 32; s <<= 1) {
+                const long long u = __shfl_up_sync(0xFFFFFFFFu, w, s);
+                if (lane >= s) w += u;
+            }
+            warp_sum[warp][lane] = w;
+        }
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            long long before = carry[k];
-            for (int w = 0; w < kPlanThreads / 32; ++w) {
-                if (w == warp) v[k] += before;
-                before += warp_sum[k][w];
-            }
-            carry[k] = before;
+            v[k] += carry[k] + (warp ? warp_sum[k][warp - 1] : 0);
+            carry[k] += warp_sum[k][31];
         }
         if (b < a.B) {
             // sums beyond 2^31 - 1 are refused below, before any is used
@@ -117,7 +124,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     if (tid == 0) cu_q[0] = cu_take[0] = cu_back[0] = 0;
     __syncthreads();
 
-    const int64_t count = *a.free_count;
     const int64_t held = count + carry[2];
     int status = bad;
     if (!status && (count < 0 || held > a.capacity)) status = 4;
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         int pos = -1;
         if (t < tokens) {
             const int b = find(cu_q, a.B, static_cast<int>(t));
-            const int c = a.cached[b];
+            const int c = held_by[b];
             pos = c + static_cast<int>(t) - cu_q[b];
             const int have = static_cast<int>((c + mask) >> a.page_shift);
             const int j = pos >> a.page_shift;
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     }
     for (int64_t p = first; p < taken; p += step) {
         const int b = find(cu_take, a.B, static_cast<int>(p));
-        const int have = static_cast<int>((a.cached[b] + mask) >> a.page_shift);
+        const int have = static_cast<int>((held_by[b] + mask) >> a.page_shift);
         a.table[b * a.max_pages + have + static_cast<int>(p) - cu_take[b]] = taken_page(static_cast<int>(p));
     }
     for (int64_t r = first; r < returned; r += step) {
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     for (int64_t b = first; b <= a.B; b += step) {
         a.cu_q[b] = ok ? cu_q[b] : 0;
         if (b < a.B) {
-            const int c = a.cached[b], n = a.fresh[b];
+            const int c = held_by[b], n = a.fresh[b];
             a.seq_lens[b] = !ok ? c : n < 0 ? 0 : c + n;
         }
     }
@@ -179,9 +185,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 }
 
 // ------------------------------------------------------------------ append, read
-// 16 channels a thread, D / 16 neighbouring lanes a row; the rows of keys come
-// first, then those of values.  Bound by the bytes: 2 D read and D / 2 + 2
-// written a row (append).
+// 16 channels a thread, D / 16 neighbouring lanes a row, the key's and the
+// value's row of a (token, head) by the same threads, so that their loads are
+// on the way together.  Bound by the bytes: 2 D read and D / 2 + 2 written a
+// row (append).  I: the type of thread numbers, 32 bits where they suffice (the
+// divisions that find a row are most of its integer work).
 constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ bool slot_ok(const Cache &c, long long slot) {
@@ -199,68 +207,76 @@ __device__ __forceinline__ int64_t row_at(const Cache &c, long long slot, int h)
     return ((id * c.heads + h) << c.page_shift) + off;
 }
 
+template <int D, class I>
 __global__ void __launch_bounds__(kRowThreads)
 append_kernel(Cache c, const uint16_t *__restrict__ k, int64_t ldk, const uint16_t *__restrict__ v,
-              int64_t ldv, const long long *__restrict__ slots, int64_t T) {
-    const int lanes = c.D / 16;
-    const int64_t half = T * c.heads * lanes, total = 2 * half;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+              int64_t ldv, const long long *__restrict__ slots, I total) {
+    constexpr int LANES = D / 16;
     const float norm = frag::norm_of(c.group);
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < total; i0 += step) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool values = i >= half;
-        const int64_t row = (values ? i - half : i) / lanes;
-        const int part = static_cast<int>(i % lanes);
-        const int64_t t = row / c.heads;
-        const int h = static_cast<int>(row % c.heads);
+    for (I i0 = static_cast<I>(blockIdx.x) * kRowThreads; i0 < total; i0 += gridDim.x * kRowThreads) {
+        const I i = i0 + threadIdx.x, row = i / LANES, t = row / c.heads;
+        const int part = static_cast<int>(i % LANES), h = static_cast<int>(row - t * c.heads);
         const long long slot = i < total ? slots[t] : -1;
         const bool live = slot_ok(c, slot);
-        float x[16] = {};
-        if (live) frag::load16((values ? v + t * ldv : k + t * ldk) + h * c.D + 16 * part, x);
-        frag::rotate16(x, c.group == 256);
-        const uint32_t amax = frag::absmax_bits(x, lanes);
-        float factor;
-        const uint16_t s = frag::block_scale(amax, norm, factor);
-        uint32_t packed[2];
-        prep::quantize_pack(x, factor, packed);
+        uint4 raw[2][2] = {};
         if (live) {
-            const int64_t at = row_at(c, slot, h);
-            uint8_t *codes = (values ? c.vc : c.kc) + at * (c.D / 2) + 8 * part;
-            *reinterpret_cast<uint2 *>(codes) = make_uint2(packed[0], packed[1]);
-            if (part == 0) (values ? c.vs : c.ks)[at] = s;
+            const uint4 *pk = reinterpret_cast<const uint4 *>(k + static_cast<int64_t>(t) * ldk + h * D + 16 * part);
+            const uint4 *pv = reinterpret_cast<const uint4 *>(v + static_cast<int64_t>(t) * ldv + h * D + 16 * part);
+            raw[0][0] = pk[0];
+            raw[0][1] = pk[1];
+            raw[1][0] = pv[0];
+            raw[1][1] = pv[1];
+        }
+        const int64_t at = live ? row_at(c, slot, h) : 0;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            float x[16], factor;
+            frag::unpack_bf16x8(raw[y][0], x);
+            frag::unpack_bf16x8(raw[y][1], x + 8);
+            frag::rotate16(x, c.group == 256);
+            const uint16_t s = frag::block_scale(frag::absmax_bits(x, LANES), norm, factor);
+            uint32_t packed[2];
+            prep::quantize_pack(x, factor, packed);
+            if (live) {
+                *reinterpret_cast<uint2 *>((y ? c.vc : c.kc) + at * (D / 2) + 8 * part) = make_uint2(packed[0], packed[1]);
+                if (part == 0) (y ? c.vs : c.ks)[at] = s;
+            }
         }
     }
 }
 
+template <int D, class I>
 __global__ void __launch_bounds__(kRowThreads)
-read_kernel(Cache c, const long long *__restrict__ slots, int64_t T, uint16_t *__restrict__ k,
+read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__restrict__ k,
             uint16_t *__restrict__ v) {
-    const int lanes = c.D / 16;
-    const int64_t half = T * c.heads * lanes, total = 2 * half;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+    constexpr int LANES = D / 16;
     const float norm = frag::norm_of(c.group);
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < total; i0 += step) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool values = i >= half;
-        const int64_t row = (values ? i - half : i) / lanes;
-        const int part = static_cast<int>(i % lanes);
-        const long long slot = i < total ? slots[row / c.heads] : -1;
-        float x[16] = {};
-        float s = 0.0f;
+    for (I i0 = static_cast<I>(blockIdx.x) * kRowThreads; i0 < total; i0 += gridDim.x * kRowThreads) {
+        const I i = i0 + threadIdx.x, row = i / LANES, t = row / c.heads;
+        const int part = static_cast<int>(i % LANES);
+        const long long slot = i < total ? slots[t] : -1;
+        uint2 w[2] = {};
+        float s[2] = {0.0f, 0.0f};
         if (slot_ok(c, slot)) {
-            const int64_t at = row_at(c, slot, static_cast<int>(row % c.heads));
-            const uint2 w = *reinterpret_cast<const uint2 *>((values ? c.vc : c.kc) + at * (c.D / 2) + 8 * part);
-            s = frag::bf16_f32((values ? c.vs : c.ks)[at]);
+            const int64_t at = row_at(c, slot, static_cast<int>(row - t * c.heads));
+            w[0] = *reinterpret_cast<const uint2 *>(c.kc + at * (D / 2) + 8 * part);
+            w[1] = *reinterpret_cast<const uint2 *>(c.vc + at * (D / 2) + 8 * part);
+            s[0] = frag::bf16_f32(c.ks[at]);
+            s[1] = frag::bf16_f32(c.vs[at]);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            float x[16];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[e] = static_cast<float>(static_cast<int>(w.x << (28 - 4 * e)) >> 28);
-                x[8 + e] = static_cast<float>(static_cast<int>(w.y << (28 - 4 * e)) >> 28);
+                x[e] = static_cast<float>(static_cast<int>(w[y].x << (28 - 4 * e)) >> 28);
+                x[8 + e] = static_cast<float>(static_cast<int>(w[y].y << (28 - 4 * e)) >> 28);
             }
+            // sums of up to 256 codes are exact, and so is their product with
+            // the 8-bit significand of the scale: one rounding, to bf16
+            frag::rotate16(x, c.group == 256);
+            if (i < total) frag::store16((y ? v : k) + static_cast<int64_t>(row) * D + 16 * part, x, s[y] * norm);
         }
-        // sums of up to 256 codes are exact, and so is their product with
-        // the 8-bit significand of the scale: one rounding, to bf16
-        frag::rotate16(x, c.group == 256);
-        if (i < total) frag::store16((values ? v : k) + row * c.D + 16 * part, x, s * norm);
     }
 }
 
@@ -1142,7 +1158,7 @@ bool set_smem(F *kernel, int bytes) {
 
 convrot_status setup(int *dev) {
     return host::device_setup(dev, [] {
-        bool ok = set_smem(plan_kernel, 3 * (CONVROT_KV4_MAX_REQUESTS + 1) * 4);
+        bool ok = set_smem(plan_kernel, 4 * (CONVROT_KV4_MAX_REQUESTS + 1) * 4);
         ok &= set_smem(attention_kernel<64, 4>, attn_smem<64, 4>());
         ok &= set_smem(attention_kernel<64, 8>, attn_smem<64, 8>());
         ok &= set_smem(attention_kernel<64, 16>, attn_smem<64, 16>());
@@ -1189,10 +1205,21 @@ convrot_status launched() {
     return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
-// Grid of a grid-stride kernel: one pass, up to eight CTAs an SM.
-unsigned row_grid(int64_t threads, int sms) {
-    const int64_t n = (threads + kRowThreads - 1) / kRowThreads;
-    return static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
+// One launch of a row kernel over T tokens: `go` gets the head dimension, the
+// number of threads in its type and the grid (up to eight CTAs an SM).
+template <class F>
+convrot_status launch_rows(const convrot_kv4_cache *c, int64_t T, int sms, F go) {
+    const int64_t total = T * c->kv_heads * (c->head_dim / 16), n = (total + kRowThreads - 1) / kRowThreads;
+    const unsigned grid = static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
+    auto with = [&](auto d) {
+        // (a thread's number stays below the total and the grid's threads)
+        if (total < (int64_t(1) << 31)) go(d, static_cast<uint32_t>(total), grid);
+        else go(d, static_cast<uint64_t>(total), grid);
+    };
+    if (c->head_dim == 64) with(std::integral_constant<int, 64>{});
+    else if (c->head_dim == 128) with(std::integral_constant<int, 128>{});
+    else with(std::integral_constant<int, 256>{});
+    return launched();
 }
 
 // Rows of a block: the smallest of 4, 8 and 16 (8 with D = 256, whose
@@ -1262,7 +1289,7 @@ convrot_status convrot_kv4_plan(const int32_t *cached, const int32_t *new_tokens
     int64_t grid = (max_tokens + kPlanThreads - 1) / kPlanThreads;
     const int sms = host::g_dev[dev].num_sms;
     grid = grid < 1 ? 1 : grid > sms ? sms : grid;
-    plan_kernel<<<static_cast<unsigned>(grid), kPlanThreads, 3 * (B + 1) * 4, stream>>>(a);
+    plan_kernel<<<static_cast<unsigned>(grid), kPlanThreads, 4 * (B + 1) * 4, stream>>>(a);
     return launched();
 }
 
@@ -1282,10 +1309,11 @@ convrot_status convrot_kv4_append(const convrot_kv4_cache *cache, const void *k_
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
                                             cache->v_scales})) != CONVROT_OK)
         return st;
-    append_kernel<<<row_grid(2 * T * width / 16, host::g_dev[dev].num_sms), kRowThreads, 0, stream>>>(
-        device_cache(cache), static_cast<const uint16_t *>(k_bf16), ldk, static_cast<const uint16_t *>(v_bf16), ldv,
-        reinterpret_cast<const long long *>(slots), T);
-    return launched();
+    return launch_rows(cache, T, host::g_dev[dev].num_sms, [&](auto d, auto total, unsigned grid) {
+        append_kernel<decltype(d)::value, decltype(total)><<<grid, kRowThreads, 0, stream>>>(
+            device_cache(cache), static_cast<const uint16_t *>(k_bf16), ldk, static_cast<const uint16_t *>(v_bf16), ldv,
+            reinterpret_cast<const long long *>(slots), total);
+    });
 }
 
 convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *slots, int64_t T,
@@ -1302,11 +1330,11 @@ convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *s
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
                                             cache->v_scales})) != CONVROT_OK)
         return st;
-    const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
-    read_kernel<<<row_grid(2 * T * width / 16, host::g_dev[dev].num_sms), kRowThreads, 0, stream>>>(
-        device_cache(cache), reinterpret_cast<const long long *>(slots), T, static_cast<uint16_t *>(k_bf16),
-        static_cast<uint16_t *>(v_bf16));
-    return launched();
+    return launch_rows(cache, T, host::g_dev[dev].num_sms, [&](auto d, auto total, unsigned grid) {
+        read_kernel<decltype(d)::value, decltype(total)><<<grid, kRowThreads, 0, stream>>>(
+            device_cache(cache), reinterpret_cast<const long long *>(slots), total, static_cast<uint16_t *>(k_bf16),
+            static_cast<uint16_t *>(v_bf16));
+    });
 }
 
 size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int kv_heads,
