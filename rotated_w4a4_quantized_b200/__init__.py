@@ -25,7 +25,9 @@ group-scaled few-token layer (``include/convrot_w4g.h``, library
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -910,7 +912,7 @@ def _dense(t, dtype, index: int) -> bool:
 
 def _call(index: int, f, *args) -> int:
     """f(*args) with CUDA device `index` as the current one."""
-    before = torch.cuda.current_device()
+    before = torch._C._cuda_getDevice()
     if before == index:
         return f(*args)
     torch.cuda.set_device(index)
@@ -964,6 +966,7 @@ def convrot_w4g_quantize_weight(w, group: int, scale_group: int, qw=None, sg=Non
     return qw, sg
 
 
+@functools.lru_cache(maxsize=256)
 def convrot_w4g_workspace_size(M: int, K: int) -> int:
     return int(lib_w4g().convrot_w4g_workspace_size(M, K))
 
@@ -989,7 +992,7 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
     N = qw.shape[0]
     L = lib_w4g()
     if workspace is None:
-        size, pw = L.convrot_w4g_workspace_size(M, K), None
+        size, pw = convrot_w4g_workspace_size(M, K), None
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
             _keep(workspace, stream)
@@ -997,8 +1000,8 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
     else:
         _need(workspace, torch.uint8, "workspace", None, x)
         size, pw = workspace.numel(), workspace.data_ptr()
-        if size < L.convrot_w4g_workspace_size(M, K):
-            raise ValueError(f"workspace holds {size} bytes, {L.convrot_w4g_workspace_size(M, K)} needed")
+        if size < convrot_w4g_workspace_size(M, K):
+            raise ValueError(f"workspace holds {size} bytes, {convrot_w4g_workspace_size(M, K)} needed")
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
     else:
@@ -1013,11 +1016,8 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
 # the INT4 cache of keys and values (include/convrot_kv4.h)
 # ---------------------------------------------------------------------------
 
-class _Kv4CacheArg(ctypes.Structure):
-    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
-                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
-                ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int), ("page", ctypes.c_int),
-                ("head_dim", ctypes.c_int), ("group", ctypes.c_int)]
+# convrot_kv4_cache: four pointers, num_pages, kv_heads, page, head_dim, group
+_kv4_cache_arg = struct.Struct("@4PqiiiI").pack
 
 
 class Kv4Cache(NamedTuple):
@@ -1038,13 +1038,12 @@ def lib_kv4() -> ctypes.CDLL:
     if _lib_kv4 is None:
         P, I64, I, SZ, F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
                             ctypes.c_float)
-        C = ctypes.POINTER(_Kv4CacheArg)
         _lib_kv4 = _load(LIB_KV4_PATH, {
             "convrot_kv4_plan": ([P, P, I64, I, P, I64, P, I64, P, I64, P, P, P, P, P, P], I),
-            "convrot_kv4_append": ([C, P, I64, P, I64, P, I64, P], I),
-            "convrot_kv4_read": ([C, P, I64, P, P, P], I),
+            "convrot_kv4_append": ([P, P, I64, P, I64, P, I64, P], I),
+            "convrot_kv4_read": ([P, P, I64, P, P, P], I),
             "convrot_kv4_attention_workspace_size": ([I64, I64, I, I, I, I64], SZ),
-            "convrot_kv4_attention": ([C, P, I64, I64, I, P, I64, P, P, I64, F, P, SZ, P, P], I),
+            "convrot_kv4_attention": ([P, P, I64, I64, I, P, I64, P, P, I64, F, P, SZ, P, P], I),
             "convrot_kv4_check_device_error": ([P], I),
         })
     return _lib_kv4
@@ -1061,7 +1060,7 @@ def convrot_kv4_new_cache(num_pages: int, kv_heads: int, page: int, head_dim: in
 
 
 def _kv4_cache(cache, group: int):
-    """(the library's struct of a cache, its device)"""
+    """(the library's struct of a cache, its device, kv_heads, page, D)"""
     kc, ks, vc, vs = cache
     index = kc.get_device()
     shape = kc.shape
@@ -1072,8 +1071,11 @@ def _kv4_cache(cache, group: int):
         _need(ks, torch.bfloat16, "k_scales", shape[:3], kc)
         _need(vc, torch.uint8, "v_codes", shape, kc)
         _need(vs, torch.bfloat16, "v_scales", shape[:3], kc)
-    return _Kv4CacheArg(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1],
-                        shape[2], 2 * shape[3], group), index
+    pages, heads, page, half = shape
+    if not 0 <= group <= 256:
+        raise ConvRotError(2, "group")
+    return (_kv4_cache_arg(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, heads, page, 2 * half,
+                           group), index, heads, page, 2 * half)
 
 
 def _need_tokens(t, name: str, heads, head_dim: int, index: int) -> int:
@@ -1154,9 +1156,9 @@ def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, pa
 def convrot_kv4_append(k, v, cache, slots, group: int, stream=None) -> None:
     """Quantise keys and values, bf16 [T, kv_heads, D], into the cache at
     slots int64 [T] (negative: skipped)."""
-    c, index = _kv4_cache(cache, group)
-    ldk = _need_tokens(k, "k", c.kv_heads, c.head_dim, index)
-    ldv = _need_tokens(v, "v", c.kv_heads, c.head_dim, index)
+    c, index, heads, _, D = _kv4_cache(cache, group)
+    ldk = _need_tokens(k, "k", heads, D, index)
+    ldv = _need_tokens(v, "v", heads, D, index)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
@@ -1169,11 +1171,11 @@ def convrot_kv4_append(k, v, cache, slots, group: int, stream=None) -> None:
 def convrot_kv4_read(cache, slots, group: int, k=None, v=None, stream=None):
     """The cached rows of slots int64 [T], rotated back: (k, v) bf16
     [T, kv_heads, D]; zeros where the slot is negative."""
-    c, index = _kv4_cache(cache, group)
+    c, index, heads, _, D = _kv4_cache(cache, group)
     kc = cache[0]
     if not _dense(slots, torch.int64, index) or slots.dim() != 1:
         _need(slots, torch.int64, "slots", (None,), kc)
-    shape = (slots.shape[0], c.kv_heads, c.head_dim)
+    shape = (slots.shape[0], heads, D)
     k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if k is None else _need(k, torch.bfloat16, "k", shape, kc)
     v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if v is None else _need(v, torch.bfloat16, "v", shape, kc)
     _check(_call(index, lib_kv4().convrot_kv4_read, c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
@@ -1181,6 +1183,7 @@ def convrot_kv4_read(cache, slots, group: int, k=None, v=None, stream=None):
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def convrot_kv4_attention_workspace_size(T: int, B: int, heads: int, kv_heads: int, head_dim: int,
                                          max_keys: int) -> int:
     return int(lib_kv4().convrot_kv4_attention_workspace_size(T, B, heads, kv_heads, head_dim, max_keys))
@@ -1193,10 +1196,10 @@ def convrot_kv4_attention(q, cache, block_table, seq_lens, cu_q, scale: float, g
     - 1, the last of its seq_lens[b] tokens, whose rows are in the cache; its
     pages are listed in block_table[b].  Without `out`, rows behind the last
     request are whatever the new tensor held."""
-    c, index = _kv4_cache(cache, group)
+    c, index, kv_heads, page, D = _kv4_cache(cache, group)
     kc = cache[0]
-    ldq = _need_tokens(q, "q", None, c.head_dim, index)
-    T, heads, D = q.shape
+    ldq = _need_tokens(q, "q", None, D, index)
+    T, heads, _ = q.shape
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
     if (B < 0 or not _dense(seq_lens, torch.int32, index) or not _dense(block_table, torch.int32, index)
             or not _dense(cu_q, torch.int32, index) or block_table.dim() != 2 or block_table.shape[0] != B
@@ -1206,7 +1209,7 @@ def convrot_kv4_attention(q, cache, block_table, seq_lens, cu_q, scale: float, g
         _need(cu_q, torch.int32, "cu_q", (B + 1,), kc)
     L = lib_kv4()
     most = block_table.shape[1]
-    size = L.convrot_kv4_attention_workspace_size(T, B, heads, c.kv_heads, D, most * c.page)
+    size = convrot_kv4_attention_workspace_size(T, B, heads, kv_heads, D, most * page)
     if workspace is None:
         workspace = torch.empty(max(1, size), dtype=torch.uint8, device=kc.device)
         _keep(workspace, stream)

@@ -65,18 +65,17 @@ __device__ __forceinline__ void codes_s8(const CodeMasks &k, uint32_t w, uint32_
     even = (w * k.sixteen) & 0xF0F0F0F0u;
 }
 
-// The codes as exact bf16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7): 0x4300
-// is 128.0 with spacing 1, so 128 + code + 8 is one XOR away and one
-// subtraction leaves the code.
-__device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t (&o)[4]) {
-    const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xC308),
-                                                  __ushort_as_bfloat16(0xC308));             // -136
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t a = ((w >> (4 * i)) & 0x000F000Fu) ^ 0x43084308u;
-        __nv_bfloat162 h = __hadd2(*reinterpret_cast<__nv_bfloat162 *>(&a), off);
-        o[i] = *reinterpret_cast<uint32_t *>(&h);
-    }
+// The codes themselves as f16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7): in
+// the low mantissa bits of 0x6400 (1024.0, spacing 1) a nibble XOR 8 reads
+// 1024 + code + 8, and one nibble further up 1024 + 16 (code + 8).
+__device__ __forceinline__ void widen_f16(const CodeMasks &k, uint32_t w, __half2 (&o)[4]) {
+    const uint32_t bias = 0x64006400u, w8 = w >> 8;
+    const __half2 low = __float2half2_rn(-1032.0f), sixteenth = __float2half2_rn(0.0625f), high = __float2half2_rn(-72.0f);
+    auto half2_of = [](uint32_t v) { return *reinterpret_cast<__half2 *>(&v); };
+    o[0] = __hadd2(half2_of(and_xor(w, k.low, k.low8 | bias)), low);
+    o[1] = __hfma2(half2_of(and_xor(w, k.high, k.high8 | bias)), sixteenth, high);
+    o[2] = __hadd2(half2_of(and_xor(w8, k.low, k.low8 | bias)), low);
+    o[3] = __hfma2(half2_of(and_xor(w8, k.high, k.high8 | bias)), sixteenth, high);
 }
 
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
@@ -84,15 +83,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -169,10 +159,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // prep kernels, so the bits are theirs.  All 32 lanes take part.
 __device__ __forceinline__ void lane_digit(float (&v)[16], int stride) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float pair = v[e] + __shfl_xor_sync(0xFFFFFFFFu, v[e], stride);
-        const float sum = pair + __shfl_xor_sync(0xFFFFFFFFu, pair, 2 * stride);
-        v[e] = __fmaf_rn(-2.0f, v[e], sum);
+    for (int e = 0; e < 16; e += 2) {
+        float p0, p1, s0, s1;
+        ptx::add2(p0, p1, v[e], v[e + 1], __shfl_xor_sync(0xFFFFFFFFu, v[e], stride), __shfl_xor_sync(0xFFFFFFFFu, v[e + 1], stride));
+        ptx::add2(s0, s1, p0, p1, __shfl_xor_sync(0xFFFFFFFFu, p0, 2 * stride), __shfl_xor_sync(0xFFFFFFFFu, p1, 2 * stride));
+        ptx::bfly2(v[e], v[e + 1], s0, s1);
     }
 }
 

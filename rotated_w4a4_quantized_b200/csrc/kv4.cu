@@ -251,6 +251,7 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
             uint16_t *__restrict__ v) {
     constexpr int LANES = D / 16;
     const float norm = frag::norm_of(c.group);
+    const frag::CodeMasks masks;
     for (I i0 = static_cast<I>(blockIdx.x) * kRowThreads; i0 < total; i0 += gridDim.x * kRowThreads) {
         const I i = i0 + threadIdx.x, row = i / LANES, t = row / c.heads;
         const int part = static_cast<int>(i % LANES);
@@ -266,15 +267,48 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
+            // Sums of up to 256 codes are whole numbers below 2048, exact in
+            // f16: two channels an operation and a shuffle.  h[4 u + i]: codes
+            // i and i + 4 of word u.
+            __half2 h[8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                __half2 o[4];
+                frag::widen_f16(masks, u ? w[y].y : w[y].x, o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[4 * u + i] = o[i];
+            }
+            const __half2 minus2 = __float2half2_rn(-2.0f);
+#pragma unroll
+            for (int u = 0; u < 8; u += 4) {   // digit 0: codes 0-3, 4-7
+                const __half2 sum = __hadd2(__hadd2(h[u], h[u + 1]), __hadd2(h[u + 2], h[u + 3]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[u + i] = __hfma2(minus2, h[u + i], sum);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {      // digit 1: both halves of both words
+                const __half2 pair = __hadd2(h[i], h[4 + i]), sum = __hadd2(pair, __lowhigh2highlow(pair));
+                h[i] = __hfma2(minus2, h[i], sum);
+                h[4 + i] = __hfma2(minus2, h[4 + i], sum);
+            }
+            auto lane_digit = [&](int stride) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 pair = __hadd2(h[i], __shfl_xor_sync(0xFFFFFFFFu, h[i], stride));
+                    h[i] = __hfma2(minus2, h[i], __hadd2(pair, __shfl_xor_sync(0xFFFFFFFFu, pair, 2 * stride)));
+                }
+            };
+            lane_digit(1);
+            if (c.group == 256) lane_digit(4);
+            // the product with the 8-bit significand of the scale is exact too:
+            // one rounding, to bf16
             float x[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = static_cast<float>(static_cast<int>(w[y].x << (28 - 4 * e)) >> 28);
-                x[8 + e] = static_cast<float>(static_cast<int>(w[y].y << (28 - 4 * e)) >> 28);
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = __half22float2(h[i]);
+                x[8 * (i >> 2) + (i & 3)] = f.x;
+                x[8 * (i >> 2) + (i & 3) + 4] = f.y;
             }
-            // sums of up to 256 codes are exact, and so is their product with
-            // the 8-bit significand of the scale: one rounding, to bf16
-            frag::rotate16(x, c.group == 256);
             if (i < total) frag::store16((y ? v : k) + static_cast<int64_t>(row) * D + 16 * part, x, s[y] * norm);
         }
     }

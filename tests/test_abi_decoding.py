@@ -91,7 +91,7 @@ def test_w4g_host_refusals():
 def cache(**over):
     v = dict(k_codes=A, k_scales=A, v_codes=A, v_scales=A, num_pages=4, kv_heads=2, page=16, head_dim=128, group=64)
     v.update(over)
-    return cr._Kv4CacheArg(*v.values())
+    return cr._kv4_cache_arg(*(x.value if isinstance(x, ctypes.c_void_p) else x or 0 for x in v.values()))
 
 
 BAD_CACHES = [(dict(group=128), 2), (dict(group=256), 3), (dict(head_dim=96), 3), (dict(head_dim=32), 3),
