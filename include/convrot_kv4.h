@@ -122,7 +122,9 @@ size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int
  * convrot_kv4_attention_workspace_size(T, B, heads, kv_heads, D,
  * max_pages * page) bytes, 256-byte aligned (CONVROT_ERR_WORKSPACE); calls that
  * use one workspace must be ordered on the GPU; it needs no initialisation.
- * scale is any finite number.  Two kernels.
+ * -2^100 <= scale <= 2^100.  Queries are held as 16-bit whole numbers, off by
+ * at most 2^-16 of their row's largest rotated value; rows below 2^-100 count
+ * as 0, rows with a NaN or an infinity give NaN.  Two kernels.
  */
 convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void *q_bf16,
                                      int64_t ldq, int64_t T, int heads, const int32_t *block_table,

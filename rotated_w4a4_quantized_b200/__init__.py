@@ -926,11 +926,14 @@ def _raw_stream(index: int, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _keep(t: torch.Tensor, stream):
-    """A workspace of this call's own: its memory is not reused before the
-    work on `stream` is done, where that is not the current stream."""
-    if stream is not None:
-        t.record_stream(stream)
+def _empty(shape, dtype, like, stream):
+    """Memory for results and workspaces of work on `stream`, from that
+    stream's pool: no earlier work on another stream still uses it, and once
+    freed it is used again behind this work only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 _lib_w4g = None
@@ -956,8 +959,8 @@ def convrot_w4g_quantize_weight(w, group: int, scale_group: int, qw=None, sg=Non
     N, K = _rows(w, torch.bfloat16, "w")
     if scale_group not in (32, 64, 128):
         raise ConvRotError(2, "convrot_w4g_quantize_weight")
-    qw = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device) if qw is None else qw
-    sg = torch.empty(N, K // scale_group, dtype=torch.bfloat16, device=w.device) if sg is None else sg
+    qw = _empty((N, K // 2), torch.uint8, w, stream) if qw is None else qw
+    sg = _empty((N, K // scale_group), torch.bfloat16, w, stream) if sg is None else sg
     _need(qw, torch.uint8, "qw", (N, K // 2), w)
     _need(sg, torch.bfloat16, "sg", (N, K // scale_group), w)
     index = w.get_device()
@@ -994,8 +997,7 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
     if workspace is None:
         size, pw = convrot_w4g_workspace_size(M, K), None
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-            _keep(workspace, stream)
+            workspace = _empty(size, torch.uint8, x, stream)
             pw = workspace.data_ptr()
     else:
         _need(workspace, torch.uint8, "workspace", None, x)
@@ -1003,7 +1005,7 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
         if size < convrot_w4g_workspace_size(M, K):
             raise ValueError(f"workspace holds {size} bytes, {convrot_w4g_workspace_size(M, K)} needed")
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, N), torch.bfloat16, x, stream)
     else:
         _need(out, torch.bfloat16, "out", (M, N), x)
     _check(_call(index, L.convrot_w4g_linear, x.data_ptr(), qw.data_ptr(), sg.data_ptr(),
@@ -1140,12 +1142,12 @@ def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, pa
         _need(free_count, torch.int32, "free_count", (1,), cached)
     if max_tokens < 0:
         raise ValueError("max_tokens is negative")
-    dev, i32 = cached.device, torch.int32
-    seq_lens = torch.empty(B, dtype=i32, device=dev)
-    cu_q = torch.empty(B + 1, dtype=i32, device=dev)
-    slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-    positions = torch.empty(max_tokens, dtype=i32, device=dev)
-    result = torch.empty(4, dtype=i32, device=dev)
+    i32 = torch.int32
+    seq_lens = _empty(B, i32, cached, stream)
+    cu_q = _empty(B + 1, i32, cached, stream)
+    slots = _empty(max_tokens, torch.int64, cached, stream)
+    positions = _empty(max_tokens, i32, cached, stream)
+    result = _empty(4, i32, cached, stream)
     _check(_call(index, lib_kv4().convrot_kv4_plan, cached.data_ptr(), new_tokens.data_ptr(), B, page,
                  block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
                  free_count.data_ptr(), max_tokens, seq_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(),
@@ -1176,8 +1178,8 @@ def convrot_kv4_read(cache, slots, group: int, k=None, v=None, stream=None):
     if not _dense(slots, torch.int64, index) or slots.dim() != 1:
         _need(slots, torch.int64, "slots", (None,), kc)
     shape = (slots.shape[0], heads, D)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if k is None else _need(k, torch.bfloat16, "k", shape, kc)
-    v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device) if v is None else _need(v, torch.bfloat16, "v", shape, kc)
+    k = _empty(shape, torch.bfloat16, kc, stream) if k is None else _need(k, torch.bfloat16, "k", shape, kc)
+    v = _empty(shape, torch.bfloat16, kc, stream) if v is None else _need(v, torch.bfloat16, "v", shape, kc)
     _check(_call(index, lib_kv4().convrot_kv4_read, c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
                  _raw_stream(index, stream)), "convrot_kv4_read")
     return k, v
@@ -1211,15 +1213,14 @@ def convrot_kv4_attention(q, cache, block_table, seq_lens, cu_q, scale: float, g
     most = block_table.shape[1]
     size = convrot_kv4_attention_workspace_size(T, B, heads, kv_heads, D, most * page)
     if workspace is None:
-        workspace = torch.empty(max(1, size), dtype=torch.uint8, device=kc.device)
-        _keep(workspace, stream)
+        workspace = _empty(max(1, size), torch.uint8, kc, stream)
     else:
         _need(workspace, torch.uint8, "workspace", None, kc)
         if workspace.numel() < size:
             raise ValueError(f"workspace holds {workspace.numel()} bytes, {size} needed")
         size = workspace.numel()
     if out is None:
-        out = torch.empty(T, heads, D, dtype=torch.bfloat16, device=kc.device)
+        out = _empty((T, heads, D), torch.bfloat16, kc, stream)
     else:
         _need(out, torch.bfloat16, "out", (T, heads, D), kc)
     _check(_call(index, L.convrot_kv4_attention, c, q.data_ptr(), ldq, T, heads, block_table.data_ptr(), most,

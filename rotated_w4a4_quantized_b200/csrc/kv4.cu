@@ -1304,10 +1304,10 @@ convrot_status convrot_kv4_plan(const int32_t *cached, const int32_t *new_tokens
                                 int64_t *slots, int32_t *positions, int32_t *result,
                                 convrot_stream_t stream) {
     const int shift = shift_of(page);
-    if (B < 1 || B > CONVROT_KV4_MAX_REQUESTS || shift < 0 || max_pages < 0 || max_pages >= (int64_t(1) << 31) ||
+    if (B < 0 || B > CONVROT_KV4_MAX_REQUESTS || shift < 0 || max_pages < 0 || max_pages >= (int64_t(1) << 31) ||
         capacity < 0 || capacity >= (int64_t(1) << 31) || max_tokens < 0 || max_tokens >= (int64_t(1) << 31))
         return CONVROT_ERR_SHAPE;
-    if (!cached || !new_tokens || !free_count || !seq_lens || !cu_q || !result || (max_pages && !block_table) ||
+    if (!free_count || !cu_q || !result || (B && (!cached || !new_tokens || !seq_lens || (max_pages && !block_table))) ||
         (capacity && !free_pages) || (max_tokens && (!slots || !positions)))
         return CONVROT_ERR_NULL;
     if (!host::aligned16({cached, new_tokens, block_table, free_pages, free_count, seq_lens, cu_q, slots, positions, result}))
@@ -1389,7 +1389,7 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
     const int D = cache->head_dim;
     if (max_pages < 0 || max_pages >= (int64_t(1) << 31) / cache->page ||
         !attn_shape_ok(T, B, heads, cache->kv_heads, D, max_pages * cache->page) ||
-        ldq < static_cast<int64_t>(heads) * D || ldq % 8 || !(scale - scale == 0.0f))
+        ldq < static_cast<int64_t>(heads) * D || ldq % 8 || !(scale <= 0x1p100f && scale >= -0x1p100f))
         return CONVROT_ERR_SHAPE;
     if (T == 0 || B == 0) return CONVROT_OK;
     if (!q_bf16 || !seq_lens || !cu_q || !out_bf16 || !workspace || (max_pages && !block_table)) return CONVROT_ERR_NULL;

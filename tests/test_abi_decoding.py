@@ -126,7 +126,7 @@ def test_kv4_host_refusals():
     assert attn(ldq=1023) == 3 and attn(ldq=1020) == 3
     assert attn(T=-1) == 3 and attn(B=8193) == 3 and attn(B=-1) == 3
     assert attn(max_pages=-1) == 3 and attn(max_pages=1 << 27) == 3
-    assert attn(scale=float("nan")) == 3 and attn(scale=float("-inf")) == 3
+    assert attn(scale=float("nan")) == 3 and attn(scale=float("-inf")) == 3 and attn(scale=1e31) == 3
     assert attn(T=0, q=None, out=None) == 0 and attn(B=0) == 0
     assert attn(ws=None) == 1 and attn(out=None) == 1 and attn(table=None) == 1
     assert attn(n=100) == 5 and attn(ws=U) == 5
@@ -135,7 +135,7 @@ def test_kv4_host_refusals():
 
     def plan(cached=A, B=2, page=16, table=A, most=4, free=A, cap=4, tokens=4, slots=A, result=A):
         return f(cached, A, B, page, table, most, free, cap, A, tokens, A, A, slots, A, result, None)
-    assert plan(B=0) == 3 and plan(B=8193) == 3 and plan(page=48) == 3 and plan(most=-1) == 3
+    assert plan(B=-1) == 3 and plan(B=8193) == 3 and plan(page=48) == 3 and plan(most=-1) == 3
     assert plan(cap=-1) == 3 and plan(tokens=-1) == 3 and plan(tokens=1 << 31) == 3
     assert plan(cached=None) == 1 and plan(table=None) == 1 and plan(free=None) == 1 and plan(slots=None) == 1
     assert plan(cached=U) == 4 and plan(result=U) == 4

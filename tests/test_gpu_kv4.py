@@ -134,7 +134,7 @@ def test_slots_outside_the_cache_are_skipped_and_reported():
 
 def run_plan(cached, new, table, free, count, page, max_tokens):
     i32 = dict(dtype=torch.int32, device="cuda")
-    tab, fr = torch.tensor(table, **i32).reshape(len(cached), -1), torch.tensor(free, **i32)
+    tab, fr = torch.tensor(table, **i32).reshape(len(cached), len(table[0]) if table else 2), torch.tensor(free, **i32)
     args = (torch.tensor(cached, **i32), torch.tensor(new, **i32), tab, fr, torch.tensor([count], **i32), page, max_tokens)
     p = cr.convrot_kv4_plan(*args)
     again = cr.convrot_kv4_plan(*args)
@@ -191,6 +191,11 @@ def test_plan_edges_and_refusals_change_nothing(case):
     got, got_table, got_free = run_plan(cached, new, table, free, count, page, tokens)
     assert want["result"][3] == status
     assert got == want and got_table == want_table and got_free == want_free
+
+
+def test_plan_without_requests():
+    got, _, _ = run_plan([], [], [], [5, 6], 2, 16, 3)
+    assert got == dict(seq_lens=[], cu_q=[0], slots=[-1] * 3, positions=[-1] * 3, result=[2, 0, 0, 0])
 
 
 # ---------------------------------------------------------------- attention
@@ -368,6 +373,29 @@ def test_attention_on_another_stream_and_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, cr.convrot_kv4_attention(*dev, 0.1, 64))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose codes lie more than 2^32 bytes into the cache."""
+    heads, page, D = 8, 128, 128
+    pages = (1 << 32) // (heads * page * D // 2) + 40
+    cache = cr.Kv4Cache(*[torch.empty(pages, heads, page, *w, dtype=d, device="cuda")
+                          for w, d in (((D // 2,), torch.uint8), ((), torch.bfloat16)) * 2])
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(300, heads, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    small = cr.convrot_kv4_new_cache(3, heads, page, D, "cuda")
+    t = torch.arange(300).cuda()
+    table = torch.tensor([[pages - 1, pages - 30, pages - 2]]).int().cuda()
+    slots = table[0].long()[t // page] * page + t % page
+    cr.convrot_kv4_append(k, v, cache, slots, 64)
+    cr.convrot_kv4_append(k, v, small, t, 64)
+    for a, b in zip(cr.convrot_kv4_read(cache, slots, 64), cr.convrot_kv4_read(small, t, 64)):
+        assert torch.equal(a, b)
+    q = torch.randn(1, 32, D, generator=g).to(torch.bfloat16).cuda()
+    lens, cu = torch.tensor([300]).int().cuda(), torch.tensor([0, 1]).int().cuda()
+    far = cr.convrot_kv4_attention(q, cache, table, lens, cu, 0.1, 64)
+    near = cr.convrot_kv4_attention(q, small, torch.tensor([[0, 1, 2]]).int().cuda(), lens, cu, 0.1, 64)
+    assert torch.equal(far, near)
 
 
 def test_empty_calls():

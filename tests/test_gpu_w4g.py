@@ -220,6 +220,21 @@ def test_streams_and_captured_replays():
         assert torch.equal(out, want)
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes of codes: the last rows equal a small call's."""
+    N, K = (1 << 32) // 16384 + 1000, 32768
+    qw = torch.empty(N, K // 2, dtype=torch.uint8, device="cuda")
+    sg = torch.full((N, K // 128), 0.01, dtype=torch.bfloat16, device="cuda")
+    x, tail, tail_sg, _ = cuda(*draw(2, K, 900, 128, seed=8))
+    qw[-900:] = tail
+    sg[-900:] = tail_sg
+    y = cr.convrot_w4g_linear(x, qw, sg, None, 64, 128)[:, -900:]
+    z = cr.convrot_w4g_linear(x, tail, tail_sg, None, 64, 128)
+    # (another number of rows a CTA: other parts of K, sums in another order)
+    t, l1 = ref.linear(ref.rotate(x.cpu().double(), 64), tail.cpu(), tail_sg.cpu(), None)
+    assert bool(((y - z).cpu().double().abs() <= 2.0 ** -7 * t.abs() + 2.0 ** -16 * l1).all())
+
+
 def test_refusals_on_the_device():
     x, qw, sg, b = cuda(*draw(2, 256, 64, 64, seed=7))
     with pytest.raises(cr.ConvRotError, match="GROUP"):
