@@ -902,8 +902,26 @@ def _load(path: str, sigs: dict) -> ctypes.CDLL:
     return L
 
 
-# The calls below are made once a layer and token, so their checks are a few
-# comparisons; only where one fails do the named checks above say which.
+# The calls below are made once a layer and step.  Their common case (results
+# and workspace of the call's own, the current stream and device) is native
+# code, the extension module _decoding (csrc/binding.cpp); it returns None where
+# an argument is not plainly right, and the code here handles the rest: given
+# buffers and streams, other devices, and the errors.
+
+_extension = None
+
+
+def _native():
+    """The extension module; raises if it has not been built."""
+    global _extension
+    if _extension is None:
+        try:
+            from . import _decoding
+        except ImportError as e:
+            raise RuntimeError("the extension module _decoding is missing: build it with "
+                               "`python -m rotated_w4a4_quantized_b200.build` (there is no fallback path)") from e
+        _extension = _decoding
+    return _extension
 
 def _dense(t, dtype, index: int) -> bool:
     """A contiguous tensor of `dtype` on CUDA device `index`."""
@@ -980,6 +998,12 @@ def convrot_w4g_linear(x, qw, sg, bias, group: int, scale_group: int, workspace=
     weights of convrot_w4g_quantize_weight (the same group and scale_group).
     group 0 takes x as it is: rotated already, or with weights that are not.
     Made for few tokens: every 16 of them read the weights once."""
+    if workspace is None and out is None and stream is None:
+        y = _native().w4g_linear(x, qw, sg, bias, group, scale_group)
+        if y is not None:
+            if y.__class__ is int:
+                raise ConvRotError(y, "convrot_w4g_linear")
+            return y
     if scale_group not in (32, 64, 128):
         raise ConvRotError(2, "convrot_w4g_linear")
     if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not _dense(x, torch.bfloat16, index := x.get_device())
@@ -1104,17 +1128,13 @@ def _need_tokens(t, name: str, heads, head_dim: int, index: int) -> int:
 class Kv4Plan:
     """What convrot_kv4_plan lays out: seq_lens int32 [B], cu_q int32 [B + 1],
     slots int64 [max_tokens], positions int32 [max_tokens] and result int32 [4]
-    = {free pages left, pages taken, new tokens, status}."""
-    __slots__ = ("seq_lens", "cu_q", "slots", "positions", "result")
+    = {free pages left, pages taken, new tokens, status}; free_count int32 [1],
+    its first value, is the next step's."""
+    __slots__ = ("seq_lens", "cu_q", "slots", "positions", "result", "free_count")
 
-    def __init__(self, seq_lens, cu_q, slots, positions, result):
+    def __init__(self, seq_lens, cu_q, slots, positions, result, free_count):
         self.seq_lens, self.cu_q, self.slots = seq_lens, cu_q, slots
-        self.positions, self.result = positions, result
-
-    @property
-    def free_count(self):
-        """int32 [1]: free pages left, the next step's free_count."""
-        return self.result[:1]
+        self.positions, self.result, self.free_count = positions, result, free_count
 
     @property
     def status(self):
@@ -1128,6 +1148,12 @@ def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, pa
     (-1 new tokens: finished, its pages go back), block_table int32
     [B, max_pages] (completed in place), free_pages int32 [capacity] (a stack of
     free_count int32 [1] page ids; returned pages are pushed in place)."""
+    if stream is None:
+        p = _native().kv4_plan(cached, new_tokens, block_table, free_pages, free_count, page, max_tokens)
+        if p is not None:
+            if p.__class__ is int:
+                raise ConvRotError(p, "convrot_kv4_plan")
+            return Kv4Plan(*p)
     index = cached.get_device()
     B = cached.shape[0] if cached.dim() == 1 else -1
     if (index < 0 or B < 0 or not _dense(cached, torch.int32, index) or not _dense(new_tokens, torch.int32, index)
@@ -1152,12 +1178,16 @@ def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, pa
                  block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
                  free_count.data_ptr(), max_tokens, seq_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(),
                  positions.data_ptr(), result.data_ptr(), _raw_stream(index, stream)), "convrot_kv4_plan")
-    return Kv4Plan(seq_lens, cu_q, slots, positions, result)
+    return Kv4Plan(seq_lens, cu_q, slots, positions, result, result[:1])
 
 
 def convrot_kv4_append(k, v, cache, slots, group: int, stream=None) -> None:
     """Quantise keys and values, bf16 [T, kv_heads, D], into the cache at
     slots int64 [T] (negative: skipped)."""
+    if stream is None:
+        st = _native().kv4_append(k, v, cache, slots, group)
+        if st is not None:
+            return _check(st, "convrot_kv4_append")
     c, index, heads, _, D = _kv4_cache(cache, group)
     ldk = _need_tokens(k, "k", heads, D, index)
     ldv = _need_tokens(v, "v", heads, D, index)
@@ -1173,6 +1203,12 @@ def convrot_kv4_append(k, v, cache, slots, group: int, stream=None) -> None:
 def convrot_kv4_read(cache, slots, group: int, k=None, v=None, stream=None):
     """The cached rows of slots int64 [T], rotated back: (k, v) bf16
     [T, kv_heads, D]; zeros where the slot is negative."""
+    if k is None and v is None and stream is None:
+        kv = _native().kv4_read(cache, slots, group)
+        if kv is not None:
+            if kv.__class__ is int:
+                raise ConvRotError(kv, "convrot_kv4_read")
+            return kv
     c, index, heads, _, D = _kv4_cache(cache, group)
     kc = cache[0]
     if not _dense(slots, torch.int64, index) or slots.dim() != 1:
@@ -1198,6 +1234,12 @@ def convrot_kv4_attention(q, cache, block_table, seq_lens, cu_q, scale: float, g
     - 1, the last of its seq_lens[b] tokens, whose rows are in the cache; its
     pages are listed in block_table[b].  Without `out`, rows behind the last
     request are whatever the new tensor held."""
+    if workspace is None and out is None and stream is None:
+        o = _native().kv4_attention(q, cache, block_table, seq_lens, cu_q, scale, group)
+        if o is not None:
+            if o.__class__ is int:
+                raise ConvRotError(o, "convrot_kv4_attention")
+            return o
     c, index, kv_heads, page, D = _kv4_cache(cache, group)
     kc = cache[0]
     ldq = _need_tokens(q, "q", None, D, index)

@@ -3,7 +3,8 @@
 variant, include/convrot_w4a16.h), libconvrot_nvfp4.so (the NVFP4
 variant, include/convrot_nvfp4.h), libconvrot_w4g.so (the group-scaled
 few-token variant, include/convrot_w4g.h) and libconvrot_kv4.so (the INT4
-cache of keys and values, include/convrot_kv4.h).
+cache of keys and values, include/convrot_kv4.h); and the extension module
+_decoding (csrc/binding.cpp), the native part of the last two's binding.
 
     python -m rotated_w4a4_quantized_b200.build [--verbose]
 
@@ -21,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 _INC = os.path.join(os.path.dirname(HERE), "include")
@@ -44,6 +46,10 @@ LIB_W4G = os.path.join(HERE, "libconvrot_w4g.so")
 SRC_KV4 = os.path.join(HERE, "csrc", "kv4.cu")
 DEPS_KV4 = [SRC_KV4, os.path.join(_INC, "convrot_kv4.h")] + _SHARED
 LIB_KV4 = os.path.join(HERE, "libconvrot_kv4.so")
+
+SRC_BINDING = os.path.join(HERE, "csrc", "binding.cpp")
+DEPS_BINDING = [SRC_BINDING, HEADER, os.path.join(_INC, "convrot_w4g.h"), os.path.join(_INC, "convrot_kv4.h")]
+LIB_BINDING = os.path.join(HERE, "_decoding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -70,7 +76,7 @@ def _stale(lib: str, deps) -> bool:
 def stale() -> bool:
     return (_stale(LIB, DEPS + [HEADER]) or _stale(LIB_W4A16, DEPS_W4A16)
             or _stale(LIB_NVFP4, DEPS_NVFP4) or _stale(LIB_W4G, DEPS_W4G)
-            or _stale(LIB_KV4, DEPS_KV4))
+            or _stale(LIB_KV4, DEPS_KV4) or _stale(LIB_BINDING, DEPS_BINDING))
 
 
 def _build_one(src: str, lib: str, verbose: bool) -> None:
@@ -80,6 +86,25 @@ def _build_one(src: str, lib: str, verbose: bool) -> None:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)
     os.replace(tmp, lib)
+
+
+def _build_binding(verbose: bool) -> None:
+    """The extension module: plain C++ against torch's headers and the two
+    libraries beside it (found through its own folder at run time; torch's own
+    libraries are loaded with torch)."""
+    import torch
+    from torch.utils import cpp_extension
+    tmp = LIB_BINDING + f".tmp{os.getpid()}"
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in cpp_extension.include_paths()), f"-I{cuda}", f"-I{sysconfig.get_paths()['include']}",
+           SRC_BINDING, "-o", tmp, f"-L{torch_lib}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           f"-L{HERE}", "-lconvrot_w4g", "-lconvrot_kv4", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, LIB_BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -95,6 +120,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         _build_one(SRC_W4G, LIB_W4G, verbose)
     if force or _stale(LIB_KV4, DEPS_KV4):
         _build_one(SRC_KV4, LIB_KV4, verbose)
+    if force or _stale(LIB_BINDING, DEPS_BINDING):
+        _build_binding(verbose)
     return LIB
 
 
@@ -105,3 +132,4 @@ if __name__ == "__main__":
     print(LIB_NVFP4)
     print(LIB_W4G)
     print(LIB_KV4)
+    print(LIB_BINDING)

@@ -53,6 +53,24 @@ def test_missing_library_raises(monkeypatch, tmp_path, attr, state, loader):
         getattr(cr, loader)()
 
 
+def test_missing_extension_raises(monkeypatch):
+    import sys
+    monkeypatch.setattr(cr, "_extension", None)
+    monkeypatch.delattr(cr, "_decoding", raising=False)
+    monkeypatch.setitem(sys.modules, cr.__name__ + "._decoding", None)
+    with pytest.raises(RuntimeError, match="no fallback"):
+        cr._native()
+
+
+def test_extension_leaves_what_is_not_plainly_right_to_python():
+    ext = cr._native()
+    x = torch.zeros(2, 2)
+    for f, n in ((ext.w4g_linear, 6), (ext.kv4_plan, 7), (ext.kv4_append, 5), (ext.kv4_read, 3), (ext.kv4_attention, 7)):
+        for args in ([], [x] * n, [x] * (n - 1), [None] * n, [(x, x, x, x)] * n, [1] * n, [x] * (n - 2) + [64, 64],
+                     [x, (x, x, x, x), x, x, x, 0.5, 64][:n], [-1] * n, [1 << 70] * n):
+            assert f(*args) is None
+
+
 def test_w4g_host_refusals():
     L = cr.lib_w4g()
     q = L.convrot_w4g_quantize_weight

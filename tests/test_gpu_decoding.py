@@ -122,6 +122,32 @@ def test_a_captured_step_replays():
     assert cr.convrot_kv4_check_device_error() == 0
 
 
+def test_native_and_python_calls_agree():
+    """A stream given by name takes the Python path of the bindings."""
+    s = torch.cuda.current_stream()
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(20, 256, generator=g).to(torch.bfloat16).cuda()
+    qw, sg = cr.convrot_w4g_quantize_weight(torch.randn(128, 256, generator=g).to(torch.bfloat16).cuda(), 64, 64)
+    b = torch.randn(128, generator=g).to(torch.bfloat16).cuda()
+    for n in (1, 20):
+        for bias in (None, b):
+            assert torch.equal(cr.convrot_w4g_linear(x[:n], qw, sg, bias, 64, 64),
+                               cr.convrot_w4g_linear(x[:n], qw, sg, bias, 64, 64, stream=s))
+    k, v = (torch.randn(20, 2, 64, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    plans, caches = [], []
+    for kw in ({}, {"stream": s}):
+        table = i32([[-1, -1], [-1, -1]])
+        p = cr.convrot_kv4_plan(i32([0, 0]), i32([17, 3]), table, i32([5, 4, 3, 2, 1, 0]), i32([6]), 16, 20, **kw)
+        cache = cr.convrot_kv4_new_cache(6, 2, 16, 64, "cuda")
+        cr.convrot_kv4_append(k, v, cache, p.slots, 64, **kw)
+        kr, vr = cr.convrot_kv4_read(cache, p.slots, 64, **kw)
+        o = cr.convrot_kv4_attention(x.unflatten(1, (4, 64)), cache, table, p.seq_lens, p.cu_q, 0.1, 64, **kw)
+        plans.append((table, p.seq_lens, p.cu_q, p.slots, p.positions, p.result, p.free_count, p.status, kr, vr, o))
+        caches.append(cache)
+    for a, c in zip(plans[0] + tuple(caches[0]), plans[1] + tuple(caches[1])):
+        assert torch.equal(a, c) and a.shape == c.shape
+
+
 def test_writes_stay_inside_their_buffers():
     g = torch.Generator().manual_seed(5)
 
