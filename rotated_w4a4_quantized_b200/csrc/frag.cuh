@@ -204,7 +204,8 @@ __device__ __forceinline__ void store16(uint16_t *p, const float (&v)[16], float
 __device__ __forceinline__ uint32_t absmax_bits(const float (&v)[16], int lanes) {
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 16; e += 2)
+        m = max(max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu), __float_as_uint(v[e + 1]) & 0x7FFFFFFFu);
     for (int s = 1; s < lanes; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
     return m;
 }
@@ -218,7 +219,7 @@ __device__ __forceinline__ uint16_t block_scale(uint32_t amax, float norm, float
         factor = 0.0f;
         return 0;
     }
-    factor = __fdiv_rn(1.0f, bf16_f32(s)) * norm;
+    factor = __frcp_rn(bf16_f32(s)) * norm;
     return s;
 }
 

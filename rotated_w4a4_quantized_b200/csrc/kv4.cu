@@ -216,17 +216,19 @@ append_kernel(Cache c, const uint16_t *__restrict__ k, int64_t ldk, const uint16
     for (I i0 = static_cast<I>(blockIdx.x) * kRowThreads; i0 < total; i0 += gridDim.x * kRowThreads) {
         const I i = i0 + threadIdx.x, row = i / LANES, t = row / c.heads;
         const int part = static_cast<int>(i % LANES), h = static_cast<int>(row - t * c.heads);
-        const long long slot = i < total ? slots[t] : -1;
-        const bool live = slot_ok(c, slot);
+        // (rows that are skipped are loaded too: nothing waits for the slot)
         uint4 raw[2][2] = {};
-        if (live) {
+        long long slot = -1;
+        if (i < total) {
             const uint4 *pk = reinterpret_cast<const uint4 *>(k + static_cast<int64_t>(t) * ldk + h * D + 16 * part);
             const uint4 *pv = reinterpret_cast<const uint4 *>(v + static_cast<int64_t>(t) * ldv + h * D + 16 * part);
-            raw[0][0] = pk[0];
-            raw[0][1] = pk[1];
-            raw[1][0] = pv[0];
-            raw[1][1] = pv[1];
+            raw[0][0] = __ldcs(pk);
+            raw[0][1] = __ldcs(pk + 1);
+            raw[1][0] = __ldcs(pv);
+            raw[1][1] = __ldcs(pv + 1);
+            slot = slots[t];
         }
+        const bool live = slot_ok(c, slot);
         const int64_t at = live ? row_at(c, slot, h) : 0;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
@@ -268,34 +270,34 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             // Sums of up to 256 codes are whole numbers below 2048, exact in
-            // f16: two channels an operation and a shuffle.  h[4 u + i]: codes
-            // i and i + 4 of word u.
+            // f16: two channels an operation and a shuffle.  h[4 u + e]: codes
+            // e and e + 4 of word u.
             __half2 h[8];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 __half2 o[4];
                 frag::widen_f16(masks, u ? w[y].y : w[y].x, o);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[4 * u + i] = o[i];
+                for (int e = 0; e < 4; ++e) h[4 * u + e] = o[e];
             }
             const __half2 minus2 = __float2half2_rn(-2.0f);
 #pragma unroll
             for (int u = 0; u < 8; u += 4) {   // digit 0: codes 0-3, 4-7
                 const __half2 sum = __hadd2(__hadd2(h[u], h[u + 1]), __hadd2(h[u + 2], h[u + 3]));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[u + i] = __hfma2(minus2, h[u + i], sum);
+                for (int e = 0; e < 4; ++e) h[u + e] = __hfma2(minus2, h[u + e], sum);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {      // digit 1: both halves of both words
-                const __half2 pair = __hadd2(h[i], h[4 + i]), sum = __hadd2(pair, __lowhigh2highlow(pair));
-                h[i] = __hfma2(minus2, h[i], sum);
-                h[4 + i] = __hfma2(minus2, h[4 + i], sum);
+            for (int e = 0; e < 4; ++e) {      // digit 1: both halves of both words
+                const __half2 pair = __hadd2(h[e], h[4 + e]), sum = __hadd2(pair, __lowhigh2highlow(pair));
+                h[e] = __hfma2(minus2, h[e], sum);
+                h[4 + e] = __hfma2(minus2, h[4 + e], sum);
             }
             auto lane_digit = [&](int stride) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const __half2 pair = __hadd2(h[i], __shfl_xor_sync(0xFFFFFFFFu, h[i], stride));
-                    h[i] = __hfma2(minus2, h[i], __hadd2(pair, __shfl_xor_sync(0xFFFFFFFFu, pair, 2 * stride)));
+                for (int e = 0; e < 8; ++e) {
+                    const __half2 pair = __hadd2(h[e], __shfl_xor_sync(0xFFFFFFFFu, h[e], stride));
+                    h[e] = __hfma2(minus2, h[e], __hadd2(pair, __shfl_xor_sync(0xFFFFFFFFu, pair, 2 * stride)));
                 }
             };
             lane_digit(1);
@@ -304,10 +306,10 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
             // one rounding, to bf16
             float x[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = __half22float2(h[i]);
-                x[8 * (i >> 2) + (i & 3)] = f.x;
-                x[8 * (i >> 2) + (i & 3) + 4] = f.y;
+            for (int e = 0; e < 8; ++e) {
+                const float2 f = __half22float2(h[e]);
+                x[8 * (e >> 2) + (e & 3)] = f.x;
+                x[8 * (e >> 2) + (e & 3) + 4] = f.y;
             }
             if (i < total) frag::store16((y ? v : k) + static_cast<int64_t>(row) * D + 16 * part, x, s[y] * norm);
         }

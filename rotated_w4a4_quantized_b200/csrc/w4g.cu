@@ -140,7 +140,7 @@ constexpr int kStageBytes = 16 * kStage / 2;
 __host__ __device__ constexpr int depth_of(int tok) { return tok == 4 ? 4 : 3; }
 __host__ __device__ constexpr int ring_bytes(int tok) { return kWarps * depth_of(tok) * kStageBytes; }
 // numbers and factors held at a time
-__host__ __device__ constexpr int act_bytes(int tok) { return 224 * 1024 - ring_bytes(tok); }
+__host__ __device__ constexpr int act_bytes(int tok) { return 226 * 1024 - ring_bytes(tok); }
 constexpr int kMaxRows = 128;                // of a CTA
 constexpr int kFusedLanes = 2 * kThreads;    // lanes of 16 channels that a CTA turns into numbers itself
 
