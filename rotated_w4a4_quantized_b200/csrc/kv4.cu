@@ -370,6 +370,7 @@ constexpr int kMaxCtas = 592;
 
 constexpr int kTile = 64;               // keys
 constexpr int kMinUnits = kAttnWarps;   // at least one tile a warp
+constexpr int kTurn = 8;                // units that a turn from one request to the next counts
 constexpr uint32_t kLeastExponent = 15;   // of a reference scale, so that 2^kUnit over it is a float
 constexpr uint32_t kUnit = 6;             // weights are at most 2^kRoom 2^kUnit 2
 constexpr float kRoom = 8.0f;
@@ -395,6 +396,7 @@ __device__ __forceinline__ int sigma(int g) { return (g & 1) ? 4 + ((g >> 1) ^ 1
 
 struct Request {
     int len, q0, nq, tiles, blocks;
+    __device__ __forceinline__ long long span() const { return static_cast<long long>(tiles) + kTurn; }
 };
 
 // Request b's sizes, clamped to what its buffers hold.
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const Request r = request_of<ROWS>(a, b);
-        mine += static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
+        mine += r.span() * r.blocks * a.c.heads;
     }
     long long incl = mine;
     for (int s = 1; s < 32; s <<= 1) {
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
         long long at = before;
         for (int b = b_lo; b < b_hi; ++b) {
             const Request r = request_of<ROWS>(a, b);
-            const long long n = static_cast<long long>(r.tiles) * r.blocks * a.c.heads;
+            const long long n = r.span() * r.blocks * a.c.heads;
             if (u0 < at + n) {
                 start_b = b;
                 start_unit = at;
@@ -532,7 +534,6 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
     const uint32_t st_s = ptx::smem_u32(st);
     const uint16_t *sks = reinterpret_cast<const uint16_t *>(st + TILE * D), *svs = sks + TILE;
     const int page_mask = (1 << a.c.page_shift) - 1, num_pages = static_cast<int>(a.c.num_pages);
-    const bool one_page = a.c.page_shift >= 6;   // a tile lies in one page
     const frag::CodeMasks masks;
     // this thread's row in a 16-key block, of its first scores
     const int key0 = sigma(g) + (HALF && t4 >= 2 ? 8 : 0);
@@ -546,81 +547,57 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
     auto locate = [&](long long u) {
         Segment sg;
         sg.rq = request_of<ROWS>(a, b);
-        long long n = static_cast<long long>(sg.rq.tiles) * sg.rq.blocks * a.c.heads;
+        long long n = sg.rq.span() * sg.rq.blocks * a.c.heads;
         while (u >= base + n && b + 1 < a.B) {
             base += n;
             sg.rq = request_of<ROWS>(a, ++b);
-            n = static_cast<long long>(sg.rq.tiles) * sg.rq.blocks * a.c.heads;
+            n = sg.rq.span() * sg.rq.blocks * a.c.heads;
         }
         const long long at = min(u - base, n - 1);   // (n is 0 only if lengths change under the kernel)
-        const int seg = n < 1 ? 0 : at < (1ll << 31) ? static_cast<int>(static_cast<unsigned>(at) / sg.rq.tiles)
-                                                     : static_cast<int>(at / sg.rq.tiles);
+        const int seg = n < 1 ? 0 : at < (1ll << 31) ? static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(sg.rq.span()))
+                                                     : static_cast<int>(at / sg.rq.span());
         sg.b = b;
-        sg.u0 = base + static_cast<long long>(seg) * sg.rq.tiles;
+        sg.u0 = base + seg * sg.rq.span();
         sg.u1 = sg.u0 + sg.rq.tiles;
-        sg.tile0 = static_cast<int>(max(u - sg.u0, 0ll));
+        sg.tile0 = static_cast<int>(min(max(u - sg.u0, 0ll), static_cast<long long>(sg.rq.tiles)));
         sg.tile1 = static_cast<int>(min(u1, sg.u1) - sg.u0);
         const int blocks = max(sg.rq.blocks, 1);
         sg.h = seg / blocks;
         sg.rb = seg % blocks;
         return sg;
     };
-            // Request a tile's keys; its values are requested once the last
-            // tile's have been read.  A copy instruction takes KPI keys' codes,
-            // 16 bytes a lane; lanes 0-7 take the scales, 8 keys each.
-            constexpr int CPK = D / 32, KPI = 32 / CPK;
-                    int ids[NB];                    // pages of the tile's 16-key blocks, -1: none
-            int in_page = 0;                // the tile's first key in its page
-    #pragma unroll
-            for (int i = 0; i < NB; ++i) ids[i] = -1;
-            auto copy = [&](int h, const uint8_t *codes, const uint16_t *scales, int i) {   // keys (0) or values (1)
-                const uint32_t dst = st_s + i * (TILE * D / 2) + 16 * lane, sdst = st_s + TILE * D + i * (TILE * 2) + 16 * lane;
-                if (one_page) {
-                    const int64_t row = ((static_cast<int64_t>(ids[0]) * a.c.heads + h) << a.c.page_shift) + in_page;
-                    const bool there = ids[0] >= 0;
-                    const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
-    #pragma unroll
-                    for (int y = 0; y < TILE / KPI; ++y)
-                        frag::cp_async16_or_zero(dst + 512 * y, there ? src + 512 * y : src, there);
-                    if (lane < 8) frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * lane : scales, there);
-                } else {
-    #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) {
-                        const int64_t row = ((static_cast<int64_t>(ids[blk]) * a.c.heads + h) << a.c.page_shift) +
-                                            ((in_page + 16 * blk) & page_mask);
-                        const bool there = ids[blk] >= 0;
-                        const uint8_t *src = there ? codes + row * (D / 2) + 16 * lane : codes;
-    #pragma unroll
-                        for (int y = 0; y < 16 / KPI; ++y)
-                            frag::cp_async16_or_zero(dst + (16 / KPI * blk + y) * 512, there ? src + 512 * y : src, there);
-                        if ((lane >> 1) == blk)
-                            frag::cp_async16_or_zero(sdst, there ? scales + row + 8 * (lane & 1) : scales, there);
-                    }
-                }
-                prep::cp_async_commit();
-            };
-            // Table entries are read a tile ahead of their use (-1 behind the
-    // request's end), and checked when they are used.
-    int ahead[NB];
-    auto look_ahead = [&](const Segment &sg, int tile) {
-        const int *row = a.table + sg.b * a.max_pages;
+    // Request a tile's keys; its values are requested once the last tile's have
+    // been read.  A page holds at least 16 keys, so a 16-key block lies in one:
+    // the 8 lanes of a block copy its codes, 128 bytes an instruction, and two
+    // of them its scales, all from the one page that the lane has looked up.
+    const int block = lane >> 3;
+    int id = -1;                        // the page of this lane's block, -1: none
+    int in_page = 0;                    // the block's first key in it
+    auto copy = [&](int h, const uint8_t *codes, const uint16_t *scales, int i) {   // keys (0) or values (1)
+        const int64_t row = ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) + in_page;
+        const bool there = id >= 0;
+        const uint8_t *src = there ? codes + row * (D / 2) + 16 * (lane & 7) : codes;
+        const uint32_t dst = st_s + i * (TILE * D / 2) + block * (16 * D / 2) + 16 * (lane & 7);
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-            if (blk && one_page) break;
-            const int64_t j0 = static_cast<int64_t>(tile) * TILE + 16 * blk;
-            ahead[blk] = j0 < sg.rq.len ? row[j0 >> a.c.page_shift] : -1;
-        }
+        for (int y = 0; y < D / 16; ++y) frag::cp_async16_or_zero(dst + 128 * y, there ? src + 128 * y : src, there);
+        if ((lane & 7) < 2)
+            frag::cp_async16_or_zero(st_s + TILE * D + i * (TILE * 2) + 32 * block + 16 * (lane & 7),
+                                     there ? scales + row + 8 * (lane & 7) : scales, there);
+        prep::cp_async_commit();
+    };
+    // Table entries are read a tile ahead of their use (-1 behind the
+    // request's end), and checked when they are used.
+    int ahead = -1;
+    auto look_ahead = [&](const Segment &sg, int tile) {
+        const int64_t j0 = static_cast<int64_t>(tile) * TILE + 16 * block;
+        ahead = j0 < sg.rq.len ? a.table[sg.b * a.max_pages + (j0 >> a.c.page_shift)] : -1;
     };
     auto request = [&](const Segment &sg, int tile) {
-        in_page = (tile * TILE) & page_mask;
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-            if (blk && one_page) break;
-            ids[blk] = ahead[blk];
-            if (ids[blk] < 0 || ids[blk] >= num_pages) {
-                ids[blk] = -1;
-                if (tile * TILE + 16 * blk < sg.rq.len && lane == 0) page_error();
-            }
+        in_page = (tile * TILE + 16 * block) & page_mask;
+        id = ahead;
+        if (id < 0 || id >= num_pages) {
+            id = -1;
+            if (tile * TILE + 16 * block < sg.rq.len && (lane & 7) == 0) page_error();
         }
         copy(sg.h, a.c.kc, a.c.ks, 0);
         look_ahead(sg, tile + kAttnWarps);
@@ -650,6 +627,11 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
     };
 
     Segment next = locate(u0);
+    if (next.tile0 == next.rq.tiles) {  // begins in a turn
+        const long long u = next.u0 + next.rq.span();
+        if (u >= u1) return;
+        next = locate(u);
+    }
     start(next);
     for (bool last = false; !last;) {
         const Segment sg = next;
@@ -743,12 +725,9 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
         for (int tile = tile0 + warp; tile < tile1; tile += kAttnWarps) {
             const int k0 = tile * TILE;
             // 16-key blocks that are there; whether every query sees every key
-            uint32_t here = 0;
-            if (one_page) here = ids[0] >= 0 ? (1u << NB) - 1 : 0u;
-            else
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk) here |= (ids[blk] >= 0 ? 1u : 0u) << blk;
-            const bool all = here == (1u << NB) - 1 && k0 + TILE - 1 <= least;
+            const bool mine_here = id >= 0;
+            const uint32_t here = __ballot_sync(0xFFFFFFFFu, mine_here);   // bit 8 blk: block blk's
+            const bool all = here == 0xFFFFFFFFu && k0 + TILE - 1 <= least;
             frag::cp_async_wait<1>();   // the keys are there, the values may be on their way
             __syncwarp();
             float s[NB][NT][NS];
@@ -830,7 +809,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
 #pragma unroll
                 for (int blk = 0; blk < NB; ++blk) {
                     const int ja = k0 + 16 * blk + key0;
-                    const bool there = (here >> blk) & 1;
+                    const bool there = (here >> (8 * blk)) & 1;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -847,10 +826,9 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             if (!all) {
                 asm volatile("");
                 // hidden and infinite scales do not count
-                const bool there = (here >> (lane >> 3)) & 1;
                 const uint32_t lo = two & 0xFFFFu, hi = two >> 16;
-                scale_bits = max(there && k0 + 2 * lane < rq.len && lo < 0x7F80u ? lo : 0u,
-                                 there && k0 + 2 * lane + 1 < rq.len && hi < 0x7F80u ? hi : 0u);
+                scale_bits = max(mine_here && k0 + 2 * lane < rq.len && lo < 0x7F80u ? lo : 0u,
+                                 mine_here && k0 + 2 * lane + 1 < rq.len && hi < 0x7F80u ? hi : 0u);
             }
             turn = scale_bits >= (ref + 1) << 7;
 #pragma unroll
@@ -930,7 +908,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
                         asm volatile("");
                         // a hidden key's scale may be anything
                         const int ja = k0 + 16 * blk + key0;
-                        const bool there = (here >> blk) & 1;
+                        const bool there = (here >> (8 * blk)) & 1;
 #pragma unroll
                         for (int x = 0; x < NS; ++x)
                             if (!there || ja + 4 * (x & 2) > cmax[nt][x & 1]) w[x] = 0.0f;
@@ -1026,7 +1004,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             else prep::cp_async_commit();
         }
         frag::cp_async_wait<0>();
-        const long long end = sg.u0 + tile1;
+        const long long end = sg.u0 + rq.span();
         last = end >= u1;
 
         // ---- join the warps

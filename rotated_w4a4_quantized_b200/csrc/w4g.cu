@@ -135,12 +135,12 @@ prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, int 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStageBytes = 16 * kStage / 2;
-// Stages of a warp's ring: with few tokens the weights' latency counts, with
-// more the room for their numbers.
-__host__ __device__ constexpr int depth_of(int tok) { return tok == 4 ? 4 : 3; }
-__host__ __device__ constexpr int ring_bytes(int tok) { return kWarps * depth_of(tok) * kStageBytes; }
+// Stages of a warp's ring, for which there is room for kRing.
+constexpr int kRing = 3;
+__host__ __device__ constexpr int depth_of(int tok, int scale_group) { return tok == 8 && scale_group == 32 ? 3 : 2; }
+constexpr int kRingBytes = kWarps * kRing * kStageBytes;
 // numbers and factors held at a time
-__host__ __device__ constexpr int act_bytes(int tok) { return 226 * 1024 - ring_bytes(tok); }
+constexpr int kActBytes = 226 * 1024 - kRingBytes;
 constexpr int kMaxRows = 128;                // of a CTA
 constexpr int kFusedLanes = 2 * kThreads;    // lanes of 16 channels that a CTA turns into numbers itself
 
@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     constexpr int NT = HALF ? 1 : TOK / 8;
     constexpr int GROUPS = kStage / SG;      // scale groups of a stage
     constexpr int STEPS = SG / 32;           // of a group
-    constexpr int kDepth = depth_of(TOK);
+    constexpr int kDepth = depth_of(TOK, SG);
+    static_assert(kDepth <= kRing);
     extern __shared__ uint4 smem[];
     __shared__ uint4 zeros;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Args a) {
     const int groups = a.K / SG;
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * (kDepth * kStageBytes);
-    uint4 *act = smem + ring_bytes(TOK) / 16;   // [slice * 32 words][pitch]
+    uint4 *act = smem + kRingBytes / 16;   // [slice * 32 words][pitch]
     float *fac = reinterpret_cast<float *>(act + a.slice * (kStage / 8) * pitch);   // [slice][pitch]
     // this lane's copies of a stage: rows lane / 8 + 0, 4, 8, 12, chunk lane % 8
     const int chunk = lane & 7, copy_row = lane >> 3;
@@ -408,7 +409,7 @@ using namespace w4g;
 template <int TOK, int SG>
 bool opt_in() {
     return cudaFuncSetAttribute(product_kernel<TOK, SG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                ring_bytes(TOK) + act_bytes(TOK)) == cudaSuccess;
+                                kRingBytes + kActBytes) == cudaSuccess;
 }
 
 convrot_status setup(int *dev) {
@@ -437,8 +438,7 @@ int64_t pitch_of(int64_t M) { return M <= 4 ? M : M <= 8 ? 8 : 16; }
 
 // Stages of numbers that the shared memory holds beside the weights' rings.
 int64_t stages_held(int64_t M) {
-    const int tok = M <= 4 ? 4 : M <= 8 ? 8 : 16;
-    return act_bytes(tok) / ((kStage * 2 + static_cast<int64_t>(sizeof(float))) * pitch_of(M));
+    return kActBytes / ((kStage * 2 + static_cast<int64_t>(sizeof(float))) * pitch_of(M));
 }
 
 // Whether every CTA of the product turns the rows into numbers itself: few
@@ -451,7 +451,7 @@ bool fused(int64_t M, int64_t K) {
 template <int TOK>
 convrot_status launch_product(const Args &a, int scale_group, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.N + a.R - 1) / a.R), static_cast<unsigned>((a.M + 15) / 16));
-    const size_t smem = ring_bytes(TOK) + a.slice * (kStage * 2 + sizeof(float)) * pitch_of(a.M);
+    const size_t smem = kRingBytes + a.slice * (kStage * 2 + sizeof(float)) * pitch_of(a.M);
     auto go = [&](auto *kernel) {
         if (!a.x) return host::launch_dependent(kernel, grid, dim3(kThreads), smem, stream, a);
         kernel<<<grid, kThreads, smem, stream>>>(a);
