@@ -152,14 +152,18 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // ---------------------------------------------------------------- rotation
-// The unnormalised rotation of 16 consecutive channels a thread, whole groups
-// in neighbouring lanes (4 lanes for n = 64, 16 for n = 256; channel order =
-// lane order).  Digits 0 and 1 run in registers, digits 2 and 3 as shuffles;
-// every quadruple is added as (x_0 + x_1) + (x_2 + x_3), the order of the
-// prep kernels, so the bits are theirs.  All 32 lanes take part.
-__device__ __forceinline__ void lane_digit(float (&v)[16], int stride) {
+// The unnormalised rotation of 16 or 32 consecutive channels a thread, whole
+// groups in neighbouring lanes (channel order = lane order): 4 or 2 lanes for
+// n = 64, 16 or 8 for n = 256.  Digits 0 and 1 run in registers, the others
+// over lanes; every quadruple is added as (x_0 + x_1) + (x_2 + x_3), the order
+// of the prep kernels, so the bits are theirs.  All 32 lanes take part.  With
+// 32 channels a thread adds half of each quadruple of digit 2 by itself: one
+// shuffle for two channels there, against two for each (16 for the whole
+// rotation of 32 channels, against 64).
+template <int E>
+__device__ __forceinline__ void lane_digit(float (&v)[E], int stride) {
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
+    for (int e = 0; e < E; e += 2) {
         float p0, p1, s0, s1;
         ptx::add2(p0, p1, v[e], v[e + 1], __shfl_xor_sync(0xFFFFFFFFu, v[e], stride), __shfl_xor_sync(0xFFFFFFFFu, v[e + 1], stride));
         ptx::add2(s0, s1, p0, p1, __shfl_xor_sync(0xFFFFFFFFu, p0, 2 * stride), __shfl_xor_sync(0xFFFFFFFFu, p1, 2 * stride));
@@ -167,11 +171,25 @@ __device__ __forceinline__ void lane_digit(float (&v)[16], int stride) {
     }
 }
 
-__device__ __forceinline__ void rotate16(float (&v)[16], bool wide) {
+__device__ __forceinline__ void rotate(float (&v)[16], bool wide) {
     prep::radix4_digit0(v);
     prep::radix4_stage<4>(v);
     lane_digit(v, 1);
     if (wide) lane_digit(v, 4);
+}
+
+__device__ __forceinline__ void rotate(float (&v)[32], bool wide) {
+    prep::radix4_digit0(v);
+    prep::radix4_stage<4>(v);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        float p0, p1, s0, s1;
+        ptx::add2(p0, p1, v[e], v[e + 1], v[16 + e], v[17 + e]);
+        ptx::add2(s0, s1, p0, p1, __shfl_xor_sync(0xFFFFFFFFu, p0, 1), __shfl_xor_sync(0xFFFFFFFFu, p1, 1));
+        ptx::bfly2(v[e], v[e + 1], s0, s1);
+        ptx::bfly2(v[16 + e], v[17 + e], s0, s1);
+    }
+    if (wide) lane_digit(v, 2);
 }
 
 // 2^-digits of the normalised matrix.
@@ -201,10 +219,11 @@ __device__ __forceinline__ void store16(uint16_t *p, const float (&v)[16], float
 
 // The largest |v| over `lanes` neighbouring lanes, as float bits: an integer
 // maximum, so that an infinity or a NaN (larger still) wins.
-__device__ __forceinline__ uint32_t absmax_bits(const float (&v)[16], int lanes) {
+template <int E>
+__device__ __forceinline__ uint32_t absmax_bits(const float (&v)[E], int lanes) {
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 16; e += 2)
+    for (int e = 0; e < E; e += 2)
         m = max(max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu), __float_as_uint(v[e + 1]) & 0x7FFFFFFFu);
     for (int s = 1; s < lanes; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
     return m;

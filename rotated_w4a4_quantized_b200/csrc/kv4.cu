@@ -185,12 +185,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 }
 
 // ------------------------------------------------------------------ append, read
-// 16 channels a thread, D / 16 neighbouring lanes a row, the key's and the
+// 32 channels a thread, D / 32 neighbouring lanes a row, the key's and the
 // value's row of a (token, head) by the same threads, so that their loads are
 // on the way together.  Bound by the bytes: 2 D read and D / 2 + 2 written a
 // row (append).  I: the type of thread numbers, 32 bits where they suffice (the
 // divisions that find a row are most of its integer work).
 constexpr int kRowThreads = 256;
+constexpr int64_t kFewChannels = 24576;   // of an SM, of the keys: below, append takes 16 a thread
 
 __device__ __forceinline__ bool slot_ok(const Cache &c, long long slot) {
     if (slot < 0) return false;
@@ -207,40 +208,43 @@ __device__ __forceinline__ int64_t row_at(const Cache &c, long long slot, int h)
     return ((id * c.heads + h) << c.page_shift) + off;
 }
 
-template <int D, class I>
-__global__ void __launch_bounds__(kRowThreads)
+// E: channels of a thread.
+template <int D, int E, class I>
+__global__ void __launch_bounds__(kRowThreads, 4)
 append_kernel(Cache c, const uint16_t *__restrict__ k, int64_t ldk, const uint16_t *__restrict__ v,
               int64_t ldv, const long long *__restrict__ slots, I total) {
-    constexpr int LANES = D / 16;
+    constexpr int LANES = D / E;
     const float norm = frag::norm_of(c.group);
     for (I i0 = static_cast<I>(blockIdx.x) * kRowThreads; i0 < total; i0 += gridDim.x * kRowThreads) {
         const I i = i0 + threadIdx.x, row = i / LANES, t = row / c.heads;
         const int part = static_cast<int>(i % LANES), h = static_cast<int>(row - t * c.heads);
         // (rows that are skipped are loaded too: nothing waits for the slot)
-        uint4 raw[2][2] = {};
+        uint4 raw[2][E / 8] = {};
         long long slot = -1;
         if (i < total) {
-            const uint4 *pk = reinterpret_cast<const uint4 *>(k + static_cast<int64_t>(t) * ldk + h * D + 16 * part);
-            const uint4 *pv = reinterpret_cast<const uint4 *>(v + static_cast<int64_t>(t) * ldv + h * D + 16 * part);
-            raw[0][0] = __ldcs(pk);
-            raw[0][1] = __ldcs(pk + 1);
-            raw[1][0] = __ldcs(pv);
-            raw[1][1] = __ldcs(pv + 1);
+            const uint4 *pk = reinterpret_cast<const uint4 *>(k + static_cast<int64_t>(t) * ldk + h * D + E * part);
+            const uint4 *pv = reinterpret_cast<const uint4 *>(v + static_cast<int64_t>(t) * ldv + h * D + E * part);
+#pragma unroll
+            for (int e = 0; e < E / 8; ++e) raw[0][e] = __ldcs(pk + e);
+#pragma unroll
+            for (int e = 0; e < E / 8; ++e) raw[1][e] = __ldcs(pv + e);
             slot = slots[t];
         }
         const bool live = slot_ok(c, slot);
         const int64_t at = live ? row_at(c, slot, h) : 0;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            float x[16], factor;
-            frag::unpack_bf16x8(raw[y][0], x);
-            frag::unpack_bf16x8(raw[y][1], x + 8);
-            frag::rotate16(x, c.group == 256);
+            float x[E], factor;
+#pragma unroll
+            for (int e = 0; e < E / 8; ++e) frag::unpack_bf16x8(raw[y][e], x + 8 * e);
+            frag::rotate(x, c.group == 256);
             const uint16_t s = frag::block_scale(frag::absmax_bits(x, LANES), norm, factor);
-            uint32_t packed[2];
+            uint32_t packed[E / 8];
             prep::quantize_pack(x, factor, packed);
             if (live) {
-                *reinterpret_cast<uint2 *>((y ? c.vc : c.kc) + at * (D / 2) + 8 * part) = make_uint2(packed[0], packed[1]);
+                uint8_t *dst = (y ? c.vc : c.kc) + at * (D / 2) + E / 2 * part;
+                if constexpr (E == 16) *reinterpret_cast<uint2 *>(dst) = make_uint2(packed[0], packed[1]);
+                else *reinterpret_cast<uint4 *>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
                 if (part == 0) (y ? c.vs : c.ks)[at] = s;
             }
         }
@@ -427,7 +431,7 @@ __device__ __forceinline__ float ex2(float x) {
 // Output row r of a row block -> rotate back 16 channels a thread and store.
 __device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, int h, int row,
                                           int part, float (&x)[16], float total) {
-    frag::rotate16(x, a.c.group == 256);
+    frag::rotate(x, a.c.group == 256);
     const int i = row / a.G;
     if (i < rq.nq) {
         const float f = total > 0.0f || total != total ? frag::norm_of(a.c.group) / total : 0.0f;
@@ -646,7 +650,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             float x[16];
             frag::unpack_bf16x8(raw[0], x);
             frag::unpack_bf16x8(raw[1], x + 8);
-            frag::rotate16(x, a.c.group == 256);
+            frag::rotate(x, a.c.group == 256);
             const uint32_t amax = frag::absmax_bits(x, LANES);
             // 16-bit whole numbers, the row's largest at 32000; rows below
             // 2^-100 count as 0, rows with a NaN or an infinity give NaN
@@ -1219,11 +1223,12 @@ convrot_status launched() {
     return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
-// One launch of a row kernel over T tokens: `go` gets the head dimension, the
-// number of threads in its type and the grid (up to eight CTAs an SM).
-template <class F>
+// One launch of a row kernel over T tokens with E channels a thread: `go` gets
+// the head dimension, the number of threads in its type and the grid (up to
+// eight CTAs an SM).
+template <int E, class F>
 convrot_status launch_rows(const convrot_kv4_cache *c, int64_t T, int sms, F go) {
-    const int64_t total = T * c->kv_heads * (c->head_dim / 16), n = (total + kRowThreads - 1) / kRowThreads;
+    const int64_t total = T * c->kv_heads * (c->head_dim / E), n = (total + kRowThreads - 1) / kRowThreads;
     const unsigned grid = static_cast<unsigned>(n < 8 * sms ? n : 8 * sms);
     auto with = [&](auto d) {
         // (a thread's number stays below the total and the grid's threads)
@@ -1323,11 +1328,16 @@ convrot_status convrot_kv4_append(const convrot_kv4_cache *cache, const void *k_
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
                                             cache->v_scales})) != CONVROT_OK)
         return st;
-    return launch_rows(cache, T, host::g_dev[dev].num_sms, [&](auto d, auto total, unsigned grid) {
-        append_kernel<decltype(d)::value, decltype(total)><<<grid, kRowThreads, 0, stream>>>(
-            device_cache(cache), static_cast<const uint16_t *>(k_bf16), ldk, static_cast<const uint16_t *>(v_bf16), ldv,
-            reinterpret_cast<const long long *>(slots), total);
-    });
+    const int sms = host::g_dev[dev].num_sms;
+    auto go = [&](auto e) {
+        constexpr int E = decltype(e)::value;
+        return launch_rows<E>(cache, T, sms, [&](auto d, auto total, unsigned grid) {
+            append_kernel<decltype(d)::value, E, decltype(total)><<<grid, kRowThreads, 0, stream>>>(
+                device_cache(cache), static_cast<const uint16_t *>(k_bf16), ldk, static_cast<const uint16_t *>(v_bf16), ldv,
+                reinterpret_cast<const long long *>(slots), total);
+        });
+    };
+    return T * width < kFewChannels * sms ? go(std::integral_constant<int, 16>{}) : go(std::integral_constant<int, 32>{});
 }
 
 convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *slots, int64_t T,
@@ -1344,7 +1354,7 @@ convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *s
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
                                             cache->v_scales})) != CONVROT_OK)
         return st;
-    return launch_rows(cache, T, host::g_dev[dev].num_sms, [&](auto d, auto total, unsigned grid) {
+    return launch_rows<16>(cache, T, host::g_dev[dev].num_sms, [&](auto d, auto total, unsigned grid) {
         read_kernel<decltype(d)::value, decltype(total)><<<grid, kRowThreads, 0, stream>>>(
             device_cache(cache), reinterpret_cast<const long long *>(slots), total, static_cast<uint16_t *>(k_bf16),
             static_cast<uint16_t *>(v_bf16));

@@ -10,28 +10,33 @@
 namespace w4g {
 
 // ------------------------------------------------------------------ weights
-// 16 channels a thread over the matrix as one line of values: a rotation group
-// (4 or 16 threads) and a scale group (2, 4 or 8 threads) never cross a row,
+// 32 channels a thread over the matrix as one line of values: a rotation group
+// (2 or 8 threads) and a scale group (1, 2 or 4 threads) never cross a row,
 // because K is a multiple of both.
 constexpr int kRowThreads = 256;
 
 __global__ void __launch_bounds__(kRowThreads)
 quantize_kernel(const uint16_t *__restrict__ w, int64_t threads, int group, int scale_group,
                 uint8_t *__restrict__ qw, uint16_t *__restrict__ sg) {
-    const int lanes = scale_group / 16;
+    const int lanes = scale_group / 32;
     const float norm = group ? frag::norm_of(group) : 1.0f;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
     for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRowThreads; i0 < threads; i0 += step) {
         const int64_t i = i0 + threadIdx.x;
-        float x[16] = {};
-        if (i < threads) frag::load16(w + 16 * i, x);
-        if (group) frag::rotate16(x, group == 256);
+        uint4 raw[4] = {};
+        if (i < threads)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) raw[e] = __ldcs(reinterpret_cast<const uint4 *>(w + 32 * i) + e);
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) frag::unpack_bf16x8(raw[e], x + 8 * e);
+        if (group) frag::rotate(x, group == 256);
         float factor;
         const uint16_t s = frag::block_scale(frag::absmax_bits(x, lanes), norm, factor);
-        uint32_t packed[2];
+        uint32_t packed[4];
         prep::quantize_pack(x, factor, packed);
         if (i < threads) {
-            *reinterpret_cast<uint2 *>(qw + 8 * i) = make_uint2(packed[0], packed[1]);
+            *reinterpret_cast<uint4 *>(qw + 16 * i) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
             if (i % lanes == 0) sg[i / lanes] = s;
         }
     }
@@ -50,7 +55,7 @@ constexpr int kLanes = kStage / 16;          // lanes of a block, 16 channels ea
 
 // The 16 channels of this lane's part of a block; whole warps call it.
 __device__ __forceinline__ void whole_numbers(float (&v)[16], int group, uint4 (&words)[2], float &factor) {
-    if (group) frag::rotate16(v, group == 256);
+    if (group) frag::rotate(v, group == 256);
     const uint32_t amax = frag::absmax_bits(v, kLanes);
     const float top = __uint_as_float(amax);
     const bool zero = amax < (27u << 23);
@@ -476,7 +481,7 @@ convrot_status convrot_w4g_quantize_weight(const void *w_bf16, int64_t N, int64_
     int dev;
     if ((st = setup(&dev)) != CONVROT_OK) return st;
     if ((st = host::check_device_ptrs(dev, {w_bf16, qw, sg_bf16})) != CONVROT_OK) return st;
-    const int64_t threads = N * (K / 16);
+    const int64_t threads = N * (K / 32);
     quantize_kernel<<<row_grid(threads, host::g_dev[dev].num_sms), kRowThreads, 0, stream>>>(
         static_cast<const uint16_t *>(w_bf16), threads, group, scale_group, qw, static_cast<uint16_t *>(sg_bf16));
     return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
