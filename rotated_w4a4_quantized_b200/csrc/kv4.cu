@@ -1104,23 +1104,43 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
     auto at = [&](int k) {   // the k-th part: the first is its CTA's second
         return a.parts + (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * (ROWS * (D + 2));
     };
-    // the group's parts, relative to the largest of their references
+    // the group's parts, kBatch on the way at a time, relative to the largest
+    // of the references so far
+    constexpr int kBatch = 2;
     float x[16] = {}, sum = 0.0f, top = -INFINITY;
     if (group < count) {
-#pragma unroll 4
-        for (int k = group; k < count; k += GROUPS) top = fmaxf(top, at(k)[2 * r]);
-        const float safe = top == -INFINITY ? 0.0f : top;
-#pragma unroll 2
-        for (int k = group; k < count; k += GROUPS) {
-            const float *p = at(k);
-            const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * r);
-            const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
-            const float4 y0 = src[0], y1 = src[1], y2 = src[2], y3 = src[3];
-            const float f = ex2(ml.x - safe);
-            sum += f * ml.y;
-            const float y[16] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w, y2.x, y2.y, y2.z, y2.w, y3.x, y3.y, y3.z, y3.w};
+#pragma unroll 1
+        for (int k0 = group; k0 < count; k0 += kBatch * GROUPS) {
+            float2 ml[kBatch];
+            float4 y[kBatch][4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] += f * y[e];
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * GROUPS;
+                const float *p = at(min(k, count - 1));
+                const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
+                ml[u] = k < count ? *reinterpret_cast<const float2 *>(p + 2 * r) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[u][e] = k < count ? src[e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            const float last = top;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u].x);
+            const float safe = top == -INFINITY ? 0.0f : top, f0 = ex2(last - safe);
+            sum *= f0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= f0;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float f = ex2(ml[u].x - safe);
+                sum += f * ml[u].y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[4 * e] += f * y[u][e].x;
+                    x[4 * e + 1] += f * y[u][e].y;
+                    x[4 * e + 2] += f * y[u][e].z;
+                    x[4 * e + 3] += f * y[u][e].w;
+                }
+            }
         }
         if (group) {
 #pragma unroll

@@ -102,6 +102,29 @@ def test_append_takes_columns_of_a_fused_projection():
     assert all(torch.equal(a, b) for a, b in zip(one, two))
 
 
+@pytest.mark.parametrize("heads,D,group", [(8, 64, 64), (5, 128, 64), (3, 256, 64), (3, 256, 256)])
+def test_append_of_many_rows_is_the_append_of_few(heads, D, group):
+    """A call of many rows spreads a row over fewer threads than a call of
+    few: the bits are the same."""
+    T, page = 4000000 // (heads * D) | 1, 64
+    g = torch.Generator(device="cuda").manual_seed(D + heads)
+    kv = torch.empty(T, 2 * heads * D + 8, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    kv[T // 2, :heads * D] = 0
+    kv[T // 3, 7] = float("inf")
+    k, v = kv[:, :heads * D].unflatten(1, (heads, D)), kv[:, heads * D:2 * heads * D].unflatten(1, (heads, D))
+    pages = T // page + 3
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:T]
+    slots[5::97] = -1
+    one, two = (to(make_cache(1, heads, page, D, seed=1)) for _ in range(2))
+    one, two = (cr.Kv4Cache(*[t.expand(pages, *t.shape[1:]).contiguous() for t in c]) for c in (one, two))
+    cr.convrot_kv4_append(k, v, one, slots, group)
+    step = -(-T // 14) * 2                     # (slots begin on 16 bytes)
+    for t in range(0, T, step):
+        cr.convrot_kv4_append(k[t:t + step], v[t:t + step], two, slots[t:t + step], group)
+    for a, b in zip(one, two):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_append_keeps_nonfinite_rows_to_themselves():
     k = torch.randn(3, 2, 64).to(torch.bfloat16).cuda()
     v = k.clone()
