@@ -9,8 +9,10 @@
  *      y = row R,  a = max|y|,  s = bf16_rne(a / 7)  (0 where below 2^-100),
  *      q = clamp(round_half_away(y * (1 / s)), -7, 7)   (fp32; s = 0: 0).
  * The scale is rounded before the codes are chosen.  A row that holds a NaN
- * or an infinity gets a scale that is not finite, and so do the results that
- * read it.  Rows live in pages of `page` tokens (16, 32, 64, 128 or 256):
+ * or an infinity, or whose sums over a group are not finite (of values beyond
+ * 2^119 they may not be), gets a scale that is not finite, and so do the
+ * results that read it.  Rows live in pages of `page` tokens (16, 32, 64, 128
+ * or 256):
  *      codes  uint8 [num_pages][kv_heads][page][D/2]  (low nibble = even
  *             channel, 4-bit two's complement),
  *      scales bf16  [num_pages][kv_heads][page],
@@ -75,7 +77,9 @@ typedef struct {
  * tokens than max_tokens; 4 a negative cached length, or a free list or table
  * whose numbers cannot be (free_count outside [0, capacity], more pages come
  * back than fit).  Running the call again on the same inputs gives the same
- * outputs: only entries that it does not read have changed.  B is at most
+ * outputs: only entries that it does not read have changed.  References are not
+ * counted: a page that several requests share must not be in the table row of a
+ * request that finishes.  B is at most
  * CONVROT_KV4_MAX_REQUESTS, page as above.  One kernel.
  */
 convrot_status convrot_kv4_plan(const int32_t *cached, const int32_t *new_tokens, int64_t B,
@@ -124,7 +128,8 @@ size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int
  * use one workspace must be ordered on the GPU; it needs no initialisation.
  * -2^100 <= scale <= 2^100.  Queries are held as 16-bit whole numbers, off by
  * at most 2^-16 of their row's largest rotated value; rows below 2^-100 count
- * as 0, rows with a NaN or an infinity give NaN.  Two kernels.
+ * as 0, rows with a NaN or an infinity give NaN, rows of values beyond 2^119
+ * may.  Two kernels.
  */
 convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void *q_bf16,
                                      int64_t ldq, int64_t T, int heads, const int32_t *block_table,

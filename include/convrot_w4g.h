@@ -19,8 +19,9 @@
  *      y[m][n] = bf16_rne( sum_b s[n][b] (sum_{k in b} xr[m][k] q[n][k])
  *                          + bias[n] ),
  * with exact sums inside a scale group and fp32 beyond.  256 channels whose
- * largest value is below 2^-100 count as 0; a row with a NaN or an infinity
- * gives NaN.
+ * largest value is below 2^-100 count as 0; a row with a NaN or an infinity,
+ * or whose sums over a group are not finite (of values beyond 2^119 they may
+ * not be), gives NaN.
  *
  * Conventions are those of convrot.h: device pointers on the current device,
  * row-major, contiguous, 16-byte aligned; the caller owns every buffer and the

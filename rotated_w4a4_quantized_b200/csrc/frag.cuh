@@ -1,13 +1,16 @@
 // frag.cuh -- register-level pieces shared by the group-scaled linear and the
-// 4-bit cache: rotation of 16 channels a thread, exact widening of packed
-// INT4 codes to f16 / bf16 pairs, and the warp-level matrix product.
+// 4-bit cache: rotation of 16 or 32 channels a thread, exact widening of packed
+// INT4 codes to int8 and f16, and the warp-level matrix products.
 //
 // Why mma.sync and not tcgen05 here: these kernels have 1 to 32 columns
 // (tokens or queries) and are bound by the bytes of the packed codes.  A
 // tcgen05 MMA reads its whole 128-row A operand from TMEM whatever its column
 // count, and the codes would have to be stored to TMEM first; the warp-level
 // product takes the widened codes straight from the registers they were
-// widened in.
+// widened in.  Measured rates of the warp-level forms, a warp instruction of
+// one sub-core: m16n8k16 f16 and m16n8k32 int8 8 cycles each, so int8 has
+// twice the rate; with up to 16 columns they are a third of a kernel's cycles
+// at most.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,14 +21,14 @@
 
 namespace frag {
 
-// Codes of one 32-bit word as f16 pairs (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7), each code offset by 8 and all
-// times 2^-24.  A nibble XOR 8 is u = code + 8, and an f16 whose bits are a
-// small whole number u is the subnormal u 2^-24, exactly, which the matrix
-// product takes at its full value: one operation a pair and one shift a word,
-// against two a pair for a conversion that removes the offset.  The second of
-// two nibbles stays where it is and counts 16 times.  Callers put the factors
-// into the other operand or the result and take 8 times the other operand's
-// sum off.
+// Codes of one 32-bit word as f16 pairs (c0, c4), 16 (c1, c5), (c2, c6),
+// 16 (c3, c7), each code offset by 8 and all times 2^-24.  A nibble XOR 8 is
+// u = code + 8, and an f16 whose bits are a small whole number u is the
+// subnormal u 2^-24, exactly, which the matrix product takes at its full value:
+// one operation a pair and one shift a word, against two a pair for a
+// conversion that removes the offset.  The second of two nibbles stays where it
+// is and counts 16 times.  Callers put the factors into the other operand or
+// the result and take 8 times the other operand's sum off.
 constexpr float kCodeUnit = 1.0f / 16777216.0f;   // 2^-24
 
 // The masks are values that the compiler cannot see: as immediates the AND and

@@ -25,11 +25,16 @@ struct Cache {
 // ------------------------------------------------------------------ plan
 // One pass of integer prefix sums over the requests, done by every CTA for
 // itself (B is at most 8192: a few loads a thread and block scans, less than a
-// second launch would cost), then a grid-stride loop
-// over the new tokens and the taken pages, each found by binary search in the
-// prefix sums in shared memory.  Nothing that one CTA writes is read by
-// another: pages that come back and go out again in the same step are read
-// from the finished request's table row, not from the stack.
+// second launch would cost), then a grid-stride loop over the new tokens and
+// the taken pages, each found by binary search in the prefix sums in shared
+// memory.  Nothing that one CTA writes is read by another: pages that come back
+// and go out again in the same step are read from the finished request's table
+// row, not from the stack.
+//
+// Bound by latency: 64 requests with a token each in 5.4 us, 1024 requests with
+// 145,000 tokens in 7.9 us (1.8 MB; 0.3 us of bytes): the launch, one load of
+// the lengths, 32-lane scans with one of the warps' sums (10.5 us with a scan of
+// 10 steps over the block), ten steps of a search and one load of a table entry.
 constexpr int kPlanThreads = 1024;
 
 struct PlanArgs {
@@ -185,13 +190,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 }
 
 // ------------------------------------------------------------------ append, read
-// 32 channels a thread, D / 32 neighbouring lanes a row, the key's and the
+// 16 or 32 channels a thread, neighbouring lanes a row, the key's and the
 // value's row of a (token, head) by the same threads, so that their loads are
-// on the way together.  Bound by the bytes: 2 D read and D / 2 + 2 written a
-// row (append).  I: the type of thread numbers, 32 bits where they suffice (the
-// divisions that find a row are most of its integer work).
+// on the way together.  I: the type of thread numbers, 32 bits where they
+// suffice (45.0 against 44.7 us below; 64-bit numbers are there for calls of
+// more than 2^31 threads).
+//
+// 16384 tokens, 8 heads of 128 (12.9 us of bytes each): append in 20.7 us
+// (4.1 TB/s), read in 17.7 us (4.8 TB/s).  Append is bound by instruction
+// issue, above all shuffles and the roundings to codes.  With 32 channels a
+// thread a row takes a quarter of the shuffles, but a call of few rows half of
+// the threads, whose latency counts: 16 channels take 26.4 us there and 32 20.7;
+// for 64 tokens, append and read, 5.5 and 6.3.  They meet at kFewChannels (4096
+// tokens: 17.5 and 17.3).  Read has no rounding and packed arithmetic, and
+// 16 channels a thread, whose stores spread over half as many lines an
+// instruction, are faster: 17.7 against 20.4 us.
 constexpr int kRowThreads = 256;
-constexpr int64_t kFewChannels = 24576;   // of an SM, of the keys: below, append takes 16 a thread
+constexpr int64_t kFewChannels = 24576;   // of the keys, an SM: below, append takes 16 a thread
 
 __device__ __forceinline__ bool slot_ok(const Cache &c, long long slot) {
     if (slot < 0) return false;
@@ -331,18 +346,18 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // Codes are the A operand of both products (16 rows an instruction against 8
 // of the B side).  K's scale goes into the scores and V's into P, in fp32.
 //
-// What bounds the loop is the integer pipe that takes the codes apart (half a
-// warp instruction a cycle), so they are converted as little as can be:
-// - K: int8, 16 times the code: two ANDs for 8 codes.  The queries are 16-bit
-//   whole numbers, the row's largest value at 32000 (off by 2^-16 of it; f16
-//   is off by 2^-11 of each value), as a high and a low byte that make two
-//   columns; the sums are exact in int32.  Up to 4 rows fill the 8 columns of
-//   one product with both bytes, and each lane then has two scores of a block
-//   instead of four.
+// Codes are converted as little as can be, for the integer pipe (half a warp
+// instruction a cycle) has most of the loop's work:
+// - K: int8, 16 times the code: two ANDs and a product for 8 codes.  The queries
+//   are 16-bit whole numbers, the row's largest value at 32000 (off by 2^-16 of
+//   it; f16 is off by 2^-11 of each value), as a high and a low byte that make
+//   two columns; the sums are exact in int32.  Up to 4 rows fill the 8 columns
+//   of one product with both bytes, and each lane then has two scores of a
+//   block instead of four.
 // - V: f16 subnormals offset by 8 (frag::codes_f16), five operations for 8
-//   codes with up to 4 rows, else six; the offset's part of the
-//   outputs, -8 times the sum of the weights, comes out of one more product
-//   with a matrix of ones and is taken off before each tile.
+//   codes with up to 4 rows, else six; the offset's part of the outputs, -8
+//   times the sum of the weights, comes out of one more product with a matrix
+//   of ones and is taken off before each tile.
 // The softmax's reference is not the running maximum but within 2^8 of it: it
 // moves, and the outputs are rescaled, only when a score is more than 8 (log2)
 // above it, so most tiles need no maximum over their lanes.  P s_v is f16
@@ -357,17 +372,38 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // Copies.  Each warp has its own place for a tile's keys and one for its
 // values (codes and scales, 64 (D + 4) bytes together), filled by its own
 // 16-byte asynchronous copies: no warp waits for another inside a request.
-// (Bulk copies take 25 instructions each, a lane at a time.)  The next tile's
-// keys are requested as soon as this one's scores are there, its values after
-// the second product: with 16 warps an SM a warp has several times the copy's
-// latency until it needs them, and registers, not bytes on the way, are what
-// is short.
+// (Bulk copies take 25 instructions each, a lane at a time: 80 us against 68.)
+// The 8 lanes that copy a block of 16 keys look its page up, so that pages of
+// any size cost the same (pages of 16: 63.2 us, against 74.6 with a lane's copies
+// spread over the blocks).  The next tile's keys are requested as soon as this
+// one's scores are there, its values after the second product: with 16 warps an
+// SM a warp has several times the copy's latency until it needs them, and
+// registers, not bytes on the way, are what is short.
 //
 // Work.  Units of one tile for one (request, head, row block) are laid out in
-// one line; CTA c takes units [c S, (c + 1) S), so ragged lengths load the
-// GPU evenly and long requests are split.  A CTA whose part ends inside a
-// request writes (max, sum, O) to the workspace and combine_kernel joins the
-// parts in their order.
+// one line, with kTurn more behind each (request, head, row block) for the turn
+// to the next: queries, joining the warps, and warps without a tile.  CTA c takes
+// an even share of the line, so ragged lengths load the GPU evenly and long
+// requests are split.  A CTA whose part ends inside a request writes (max, sum,
+// O) to the workspace and combine_kernel joins the parts in their order.
+//
+// Measured (CUDA graphs), 64 requests of 1500 to 8192 keys, 32 query heads on 8
+// of 128: 59.4 us for 268 MB, 4.5 TB/s (41.1 us at the copy rate; the copies
+// alone, without arithmetic, took 63.7 us when all of it took 65).  A steady loop of the same copies
+// reads 6.1 TB/s; what is missing is the start (6.4 us to the first keys: launch,
+// prefix of the lengths, table, latency), uneven ends (CTAs end 7 us after the
+// mean) and the joining kernel (4 us).  2 requests of up to 131072 keys, 64 heads
+// on 8: 58.6 us, 4.2 TB/s.  16 requests of up to 3001 keys, 5 queries, 16 heads
+// on 4 of 256: 25.9 us, latency of few tiles a warp.
+//
+// Choices, each with both sides measured on the first case, us:
+// - rows of a block (block_rows): 59.4 with 4, 72 with 8, 112 with 16; 8 heads
+//   on a shared one (8 rows): 115 with 4, 72 with 8; 4 queries of 4 heads: 182
+//   with 4, 112 with 8 and 16.  (All before kTurn.)
+// - kTurn: 63.0 with 0, 60.6 with 4, 59.6 with 8, 60.6 with 12; the 16 requests
+//   32.9, 27.2, 25.2, 26.8.
+// - outputs_beside: outputs beside the tiles 64.5, in their place 65.2.
+// - four CTAs an SM (128 registers) 64.5, five or six (spills) 70 and 78.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxCtas = 592;
@@ -580,13 +616,14 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
     auto copy = [&](int h, const uint8_t *codes, const uint16_t *scales, int i) {   // keys (0) or values (1)
         const int64_t row = ((static_cast<int64_t>(id) * a.c.heads + h) << a.c.page_shift) + in_page;
         const bool there = id >= 0;
-        const uint8_t *src = there ? codes + row * (D / 2) + 16 * (lane & 7) : codes;
+        // (copies of no bytes name the cache's first block)
+        const uint8_t *src = codes + (there ? row * (D / 2) : 0) + 16 * (lane & 7);
+        const uint16_t *ssrc = scales + (there ? row : 0) + 8 * (lane & 7);
         const uint32_t dst = st_s + i * (TILE * D / 2) + block * (16 * D / 2) + 16 * (lane & 7);
 #pragma unroll
-        for (int y = 0; y < D / 16; ++y) frag::cp_async16_or_zero(dst + 128 * y, there ? src + 128 * y : src, there);
+        for (int y = 0; y < D / 16; ++y) frag::cp_async16_or_zero(dst + 128 * y, src + 128 * y, there);
         if ((lane & 7) < 2)
-            frag::cp_async16_or_zero(st_s + TILE * D + i * (TILE * 2) + 32 * block + 16 * (lane & 7),
-                                     there ? scales + row + 8 * (lane & 7) : scales, there);
+            frag::cp_async16_or_zero(st_s + TILE * D + i * (TILE * 2) + 32 * block + 16 * (lane & 7), ssrc, there);
         prep::cp_async_commit();
     };
     // Table entries are read a tile ahead of their use (-1 behind the
@@ -1088,6 +1125,11 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
 // CTA c joins the parts of the request that CTA c of attention_kernel began
 // and did not end: 16 channels of a row a thread, the parts dealt out to the
 // groups of ROWS D / 16 threads that the CTA has, which are joined at the end.
+// Bound by latency (about 4 us behind the attention; a launch of its own costs
+// less than a count of arrivals and the last CTA joining: 69 and 74 us for the
+// two long cases).  256 threads with 64 registers fit into the place of one
+// attention CTA that has ended: two parts on the way a thread give 59.4 us, four
+// (76 registers) 60.8, 512 threads 66.9.
 constexpr int kCombineThreads = 256;
 
 template <int D, int ROWS>
@@ -1419,9 +1461,9 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
                seq_lens, cu_q, static_cast<int>(B), scale * 1.4426950408889634f, static_cast<int4 *>(workspace),
                reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + host::round256(ctas * sizeof(int4))),
                static_cast<uint16_t *>(out_bf16)};
-    if (!cache->num_pages) {   // copies of no bytes still name an address
-        a.c.kc = a.c.vc = static_cast<uint8_t *>(const_cast<void *>(q_bf16));
-        a.c.ks = a.c.vs = static_cast<uint16_t *>(const_cast<void *>(q_bf16));
+    if (!cache->num_pages) {   // copies of no bytes still name a block's addresses: the workspace holds more
+        a.c.kc = a.c.vc = static_cast<uint8_t *>(workspace);
+        a.c.ks = a.c.vs = static_cast<uint16_t *>(workspace);
     }
     const int sms = host::g_dev[dev].num_sms;
     auto go = [&](auto d) {

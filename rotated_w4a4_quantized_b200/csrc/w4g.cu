@@ -13,6 +13,11 @@ namespace w4g {
 // 32 channels a thread over the matrix as one line of values: a rotation group
 // (2 or 8 threads) and a scale group (1, 2 or 4 threads) never cross a row,
 // because K is a multiple of both.
+//
+// Runs once a model.  4096 -> 14336 in 37.7 us with groups of 64, 3.9 TB/s of
+// reads and writes, bound by the instructions of rotation and rounding (31.7 us,
+// 4.7 TB/s, without a rotation).  16 channels a thread need four times the
+// shuffles: 52.6 us.
 constexpr int kRowThreads = 256;
 
 __global__ void __launch_bounds__(kRowThreads)
@@ -91,7 +96,9 @@ __device__ __forceinline__ void load_part(const uint16_t *x, int64_t m, int K, i
 __device__ __forceinline__ int place(int word, int row, int pitch) { return pitch >= 8 ? row ^ ((word & 3) << 1) : row; }
 
 // Numbers [block][word][pitch] and factors [block][pitch] of every 16 rows, as
-// the product holds them.
+// the product holds them.  16 channels a thread: 16 rows of 4096 are 4096
+// threads, less than one CTA an SM, so that latency is all that counts (about
+// 2.5 us, much of it behind the product's start).
 __global__ void __launch_bounds__(kRowThreads)
 prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, int pitch, uint4 *__restrict__ numbers,
                float *__restrict__ factors) {
@@ -130,17 +137,38 @@ prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, int 
 // One CTA has R consecutive rows (R spreads N over the SMs) and all of K.  Its
 // warps are (tile of 16 rows, part of K): part p of kp takes the 256-code
 // stages p, p + kp, ..., each copied to the warp's own ring in shared memory
-// with cp.async (16 rows x 128 bytes a stage; no barrier between warps).  16-byte chunk c of row r lies at c ^ (r mod 8), so the reads of one
-// word from each of 8 rows spread over all banks.  In step j of a stage lane
-// (g, t) has word 4 j + t of rows g and g + 8: the 32 channels of a step are
-// consecutive, so scale groups of 32 and more never share an accumulator.
+// with cp.async (16 rows x 128 bytes a stage; no barrier between warps).
+// 16-byte chunk c of row r lies at c ^ (r mod 8), so the reads of one word from
+// each of 8 rows spread over all banks.  In step j of a stage lane (g, t) has
+// word 4 j + t of rows g and g + 8: the 32 channels of a step are consecutive,
+// so scale groups of 32 and more never share an accumulator.
 //
-// With few tokens every CTA turns the rows into numbers itself while its first
-// weights are on their way; with more, prepare_kernel does it once.
+// Measured (4096 -> 14336, 4.8 us of bytes; CUDA graphs): one token with scale
+// groups of 64 in 10.4 us (3.0 TB/s), 16 with groups of 128 in 15.0, of which
+// prepare_kernel is 2.5; 12288 -> 8197 (8.7 us of bytes), 5 tokens, groups of
+// 32, in 20.4 (2.8 TB/s).  About 5 us of the first are the launch, the rows'
+// numbers and the first copies' latency; then the loop's instructions bound it,
+// half an instruction a cycle and sub-core: taking the codes apart and, with
+// small scale groups, turning int32 sums into fp32 and scaling them.  bf16
+// codes and activations took 17.8 us for one token and 31 for 16.
+//
+// Choices, each with both sides measured on the first layer, us:
+// - columns (TOK 4, 8, 16: the smallest that holds the tokens).  One token
+//   10.5 with 4, 11.4 with 8, 14.1 with 16; 8 tokens 13.0 with 8, 15.9 with 16.
+// - the rows' numbers.  Few rows are turned into numbers by every CTA while its
+//   first weights are on their way, more by prepare_kernel once.  Two tokens
+//   11.2 in the product, 12.3 with prepare_kernel; 5 tokens 14.1 and 12.5.  They
+//   meet at kFusedLanes (4 tokens: 12.7 and 12.4; 1024 -> 4096, 8 tokens: 4.3
+//   and 5.0).
+// - stages of a ring (depth_of): one on its way while one is used is enough
+//   for 16 warps, and more only delay the activations' loads.  One token 10.3
+//   with 2, 10.4 with 3, 10.7 with 4; 16 tokens 15.0, 15.6, 15.6.  But 5 tokens
+//   with scale groups of 32 take 13.7 with 2 and 12.6 with 3.
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStageBytes = 16 * kStage / 2;
-// Stages of a warp's ring, for which there is room for kRing.
+// Stages of a warp's ring; there is room for kRing of them in every variant, so
+// that what else fits does not depend on it.
 constexpr int kRing = 3;
 __host__ __device__ constexpr int depth_of(int tok, int scale_group) { return tok == 8 && scale_group == 32 ? 3 : 2; }
 constexpr int kRingBytes = kWarps * kRing * kStageBytes;
