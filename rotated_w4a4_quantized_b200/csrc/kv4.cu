@@ -388,18 +388,19 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // O) to the workspace and combine_kernel joins the parts in their order.
 //
 // Measured (CUDA graphs), 64 requests of 1500 to 8192 keys, 32 query heads on 8
-// of 128: 59.4 us for 268 MB, 4.5 TB/s (41.1 us at the copy rate; the copies
+// of 128: 58.0 us for 268 MB, 4.6 TB/s (41.1 us at the copy rate; the copies
 // alone, without arithmetic, took 63.7 us when all of it took 65).  A steady loop of the same copies
 // reads 6.1 TB/s; what is missing is the start (6.4 us to the first keys: launch,
 // prefix of the lengths, table, latency), uneven ends (CTAs end 7 us after the
 // mean) and the joining kernel (4 us).  2 requests of up to 131072 keys, 64 heads
-// on 8: 58.6 us, 4.2 TB/s.  16 requests of up to 3001 keys, 5 queries, 16 heads
-// on 4 of 256: 25.9 us, latency of few tiles a warp.
+// on 8: 56.9 us, 4.3 TB/s.  16 requests of up to 3001 keys, 5 queries, 16 heads
+// on 4 of 256: 25.5 us, latency of few tiles a warp.
 //
 // Choices, each with both sides measured on the first case, us:
-// - rows of a block (block_rows): 59.4 with 4, 72 with 8, 112 with 16; 8 heads
+// - rows of a block (block_rows): 64.5 with 4, 72 with 8, 112 with 16; 8 heads
 //   on a shared one (8 rows): 115 with 4, 72 with 8; 4 queries of 4 heads: 182
-//   with 4, 112 with 8 and 16.  (All before kTurn.)
+//   with 4, 112 with 8 and 16.  (All of them, and the two last lines, at a time
+//   when the first case took 64.5.)
 // - kTurn: 63.0 with 0, 60.6 with 4, 59.6 with 8, 60.6 with 12; the 16 requests
 //   32.9, 27.2, 25.2, 26.8.
 // - outputs_beside: outputs beside the tiles 64.5, in their place 65.2.
