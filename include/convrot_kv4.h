@@ -26,10 +26,11 @@
  *
  * Conventions are those of convrot.h (device pointers on the current device,
  * 16-byte aligned, caller-owned buffers, arguments validated before any
- * launch, deterministic results).  What lies in device memory cannot be
- * validated by the host: a slot or page id outside the cache, where a call
- * reads one, is skipped as if the token were not there, and recorded as
- * CONVROT_ERR_PAGE, which convrot_kv4_check_device_error reports.
+ * launch, deterministic results).  A buffer that a call writes overlaps no
+ * other that it writes or reads (CONVROT_ERR_OVERLAP).  What lies in device
+ * memory cannot be validated by the host: a slot or page id outside the cache,
+ * where a call reads one, is skipped as if the token were not there, and
+ * recorded as CONVROT_ERR_PAGE, which convrot_kv4_check_device_error reports.
  */
 #ifndef CONVROT_KV4_H_
 #define CONVROT_KV4_H_

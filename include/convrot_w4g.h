@@ -27,7 +27,8 @@
  * row-major, contiguous, 16-byte aligned; the caller owns every buffer and the
  * library allocates nothing; work is enqueued on `stream`; arguments are
  * validated before any launch; M = 0 or N = 0 is a no-op; results are
- * deterministic.  64 <= K <= CONVROT_MAX_K, K a multiple of 64, of `group`
+ * deterministic.  A buffer that a call writes overlaps no other
+ * (CONVROT_ERR_OVERLAP).  64 <= K <= CONVROT_MAX_K, K a multiple of 64, of `group`
  * where that is not 0, and of scale_group.  CONVROT_ERR_GROUP: group is not
  * 0, 64 or 256, or scale_group is not 32, 64 or 128.
  */

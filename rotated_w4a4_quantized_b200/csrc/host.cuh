@@ -82,6 +82,27 @@ inline convrot_status check_device_ptrs(int dev, std::initializer_list<const voi
     return CONVROT_OK;
 }
 
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// Whether a buffer that a call writes shares bytes with another that it writes
+// or reads.
+inline bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    auto meet = [](const Span &a, const Span &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uint64_t>(b.bytes) && y < x + static_cast<uint64_t>(a.bytes);
+    };
+    for (const Span *a = written.begin(); a != written.end(); ++a) {
+        for (const Span *b = a + 1; b != written.end(); ++b)
+            if (meet(*a, *b)) return true;
+        for (const Span &b : read)
+            if (meet(*a, b)) return true;
+    }
+    return false;
+}
+
 inline size_t round256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 // A launch that may start while the previous kernel of the stream finishes

@@ -1276,6 +1276,12 @@ convrot_status check_cache_ptrs(const convrot_kv4_cache *c) {
     return host::aligned16({c->k_codes, c->k_scales, c->v_codes, c->v_scales}) ? CONVROT_OK : CONVROT_ERR_ALIGN;
 }
 
+// Bytes of a cache's codes, of its scales, and of T tokens of `row` values with
+// ld values between them.
+int64_t code_bytes(const convrot_kv4_cache *c) { return c->num_pages * c->kv_heads * c->page * (c->head_dim / 2); }
+int64_t scale_bytes(const convrot_kv4_cache *c) { return c->num_pages * c->kv_heads * c->page * 2; }
+int64_t token_bytes(int64_t T, int64_t ld, int64_t row) { return ((T - 1) * ld + row) * 2; }
+
 Cache device_cache(const convrot_kv4_cache *c) {
     return Cache{c->k_codes, static_cast<uint16_t *>(c->k_scales), c->v_codes,
                  static_cast<uint16_t *>(c->v_scales), c->num_pages, c->kv_heads,
@@ -1366,6 +1372,10 @@ convrot_status convrot_kv4_plan(const int32_t *cached, const int32_t *new_tokens
     if ((st = host::check_device_ptrs(dev, {cached, new_tokens, block_table, free_pages, free_count, seq_lens, cu_q,
                                             slots, positions, result})) != CONVROT_OK)
         return st;
+    if (host::overlap({{block_table, B * max_pages * 4}, {free_pages, capacity * 4}, {seq_lens, B * 4}, {cu_q, (B + 1) * 4},
+                       {slots, max_tokens * 8}, {positions, max_tokens * 4}, {result, 16}},
+                      {{cached, B * 4}, {new_tokens, B * 4}, {free_count, 4}}))
+        return CONVROT_ERR_OVERLAP;
     PlanArgs a{cached, new_tokens, static_cast<int>(B), shift, block_table, max_pages, free_pages, capacity,
                free_count, max_tokens, seq_lens, cu_q, reinterpret_cast<long long *>(slots), positions, result};
     int64_t grid = (max_tokens + kPlanThreads - 1) / kPlanThreads;
@@ -1391,6 +1401,10 @@ convrot_status convrot_kv4_append(const convrot_kv4_cache *cache, const void *k_
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
                                             cache->v_scales})) != CONVROT_OK)
         return st;
+    if (host::overlap({{cache->k_codes, code_bytes(cache)}, {cache->k_scales, scale_bytes(cache)},
+                       {cache->v_codes, code_bytes(cache)}, {cache->v_scales, scale_bytes(cache)}},
+                      {{k_bf16, token_bytes(T, ldk, width)}, {v_bf16, token_bytes(T, ldv, width)}, {slots, T * 8}}))
+        return CONVROT_ERR_OVERLAP;
     const int sms = host::g_dev[dev].num_sms;
     auto go = [&](auto e) {
         constexpr int E = decltype(e)::value;
@@ -1417,6 +1431,11 @@ convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *s
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
                                             cache->v_scales})) != CONVROT_OK)
         return st;
+    const int64_t bytes = T * cache->kv_heads * cache->head_dim * 2;
+    if (host::overlap({{k_bf16, bytes}, {v_bf16, bytes}},
+                      {{cache->k_codes, code_bytes(cache)}, {cache->k_scales, scale_bytes(cache)},
+                       {cache->v_codes, code_bytes(cache)}, {cache->v_scales, scale_bytes(cache)}, {slots, T * 8}}))
+        return CONVROT_ERR_OVERLAP;
     return launch_rows<16>(cache, T, host::g_dev[dev].num_sms, [&](auto d, auto total, unsigned grid) {
         read_kernel<decltype(d)::value, decltype(total)><<<grid, kRowThreads, 0, stream>>>(
             device_cache(cache), reinterpret_cast<const long long *>(slots), total, static_cast<uint16_t *>(k_bf16),
@@ -1447,7 +1466,8 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
     if (T == 0 || B == 0) return CONVROT_OK;
     if (!q_bf16 || !seq_lens || !cu_q || !out_bf16 || !workspace || (max_pages && !block_table)) return CONVROT_ERR_NULL;
     if ((st = check_cache_ptrs(cache)) != CONVROT_OK) return st;
-    if (ws_bytes < convrot_kv4_attention_workspace_size(T, B, heads, cache->kv_heads, D, max_pages * cache->page) ||
+    const size_t need = convrot_kv4_attention_workspace_size(T, B, heads, cache->kv_heads, D, max_pages * cache->page);
+    if (ws_bytes < need ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return CONVROT_ERR_WORKSPACE;
     if (!host::aligned16({q_bf16, block_table, seq_lens, cu_q, out_bf16})) return CONVROT_ERR_ALIGN;
@@ -1456,6 +1476,11 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
     if ((st = host::check_device_ptrs(dev, {q_bf16, block_table, seq_lens, cu_q, out_bf16, workspace, cache->k_codes,
                                             cache->k_scales, cache->v_codes, cache->v_scales})) != CONVROT_OK)
         return st;
+    if (host::overlap({{out_bf16, T * heads * D * 2}, {workspace, static_cast<int64_t>(need)}},
+                      {{q_bf16, token_bytes(T, ldq, static_cast<int64_t>(heads) * D)}, {block_table, B * max_pages * 4},
+                       {seq_lens, B * 4}, {cu_q, (B + 1) * 4}, {cache->k_codes, code_bytes(cache)},
+                       {cache->k_scales, scale_bytes(cache)}, {cache->v_codes, code_bytes(cache)}, {cache->v_scales, scale_bytes(cache)}}))
+        return CONVROT_ERR_OVERLAP;
     const int G = heads / cache->kv_heads, rows = block_rows(T, B, G, D);
     const int64_t ctas = attn_ctas(T, B, G, cache->kv_heads, rows, max_pages * cache->page);
     AttnArgs a{device_cache(cache), static_cast<const uint16_t *>(q_bf16), ldq, T, G, block_table, max_pages,

@@ -509,6 +509,7 @@ convrot_status convrot_w4g_quantize_weight(const void *w_bf16, int64_t N, int64_
     int dev;
     if ((st = setup(&dev)) != CONVROT_OK) return st;
     if ((st = host::check_device_ptrs(dev, {w_bf16, qw, sg_bf16})) != CONVROT_OK) return st;
+    if (host::overlap({{qw, N * K / 2}, {sg_bf16, N * (K / scale_group) * 2}}, {{w_bf16, N * K * 2}})) return CONVROT_ERR_OVERLAP;
     const int64_t threads = N * (K / 32);
     quantize_kernel<<<row_grid(threads, host::g_dev[dev].num_sms), kRowThreads, 0, stream>>>(
         static_cast<const uint16_t *>(w_bf16), threads, group, scale_group, qw, static_cast<uint16_t *>(sg_bf16));
@@ -537,6 +538,9 @@ convrot_status convrot_w4g_linear(const void *x_bf16, const uint8_t *qw, const v
     if ((st = setup(&dev)) != CONVROT_OK) return st;
     if ((st = host::check_device_ptrs(dev, {x_bf16, qw, sg_bf16, bias_bf16, y_bf16, need ? workspace : nullptr})) != CONVROT_OK)
         return st;
+    if (host::overlap({{y_bf16, M * N * 2}, {need ? workspace : nullptr, static_cast<int64_t>(need)}},
+                      {{x_bf16, M * K * 2}, {qw, N * K / 2}, {sg_bf16, N * (K / scale_group) * 2}, {bias_bf16, N * 2}}))
+        return CONVROT_ERR_OVERLAP;
     const int sms = host::g_dev[dev].num_sms;
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
     const int64_t blocks = (K + kStage - 1) / kStage, pitch = pitch_of(M), places = (M + 15) / 16 * pitch;

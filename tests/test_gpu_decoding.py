@@ -3,6 +3,10 @@ tokens, projects them with group-scaled weights, appends keys and values to the
 cache, attends over it and projects the result.  Each operator is checked
 against its own definition on what the one before it gave, with the gates of
 their own tests, and a captured step replays."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -146,6 +150,72 @@ def test_native_and_python_calls_agree():
         caches.append(cache)
     for a, c in zip(plans[0] + tuple(caches[0]), plans[1] + tuple(caches[1])):
         assert torch.equal(a, c) and a.shape == c.shape
+
+
+def test_overlapping_buffers_are_refused():
+    """Results in the place of an operand would depend on which part of the GPU
+    is first: every such call is refused and writes nothing."""
+    def refused(f, *a, **k):
+        with pytest.raises(cr.ConvRotError, match="OVERLAP"):
+            f(*a, **k)
+    cache = cr.convrot_kv4_new_cache(4, 2, 16, 64, "cuda")
+    q = torch.randn(8, 4, 64).to(torch.bfloat16).cuda()
+    before, i32 = q.clone(), lambda v: torch.tensor(v, dtype=torch.int32).cuda()
+    table, lens, cu = i32([[0, 1, 2]]), i32([40]), i32([0, 8])
+    refused(cr.convrot_kv4_attention, q, cache, table, lens, cu, 0.1, 64, out=q)
+    room = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    out = room[4096:4096 + q.numel() * 2].view(torch.bfloat16).view(q.shape)
+    refused(cr.convrot_kv4_attention, q, cache, table, lens, cu, 0.1, 64, workspace=room, out=out)
+    slots = torch.arange(8).cuda()
+    k = torch.empty(8, 2, 64, dtype=torch.bfloat16, device="cuda")
+    refused(cr.convrot_kv4_read, cache, slots, 64, k=k, v=k)
+    same = cr.Kv4Cache(cache.k_codes, cache.k_scales, cache.k_codes, cache.v_scales)
+    refused(cr.convrot_kv4_append, q[:, :2], q[:, 2:], same, slots, 64)
+    x = q.view(8, 256)
+    weights = torch.zeros(256, 128, dtype=torch.uint8, device="cuda"), torch.zeros(256, 4, dtype=torch.bfloat16, device="cuda")
+    refused(cr.convrot_w4g_linear, x, *weights, None, 64, 64, out=x)
+    refused(cr.convrot_w4g_quantize_weight, x, 64, 64, qw=x.view(torch.uint8).view(-1)[:1024].view(8, 128))
+    pages = torch.arange(12, dtype=torch.int32, device="cuda")
+    refused(cr.convrot_kv4_plan, i32([3]), i32([1]), pages[:4].view(1, 4), pages, i32([8]), 16, 4)
+    # columns of one buffer do not overlap
+    both = torch.randn(8, 8, 64).to(torch.bfloat16).cuda()
+    cr.convrot_kv4_append(both[:, :2], both[:, 2:4], cache, slots, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(q, before) and torch.equal(pages, torch.arange(12, dtype=torch.int32, device="cuda"))
+
+
+def test_the_first_calls_may_be_captured():
+    """A process whose first calls are in a capture: nothing is set up in a
+    way that a capture forbids."""
+    code = """if True:
+        import torch
+        import rotated_w4a4_quantized_b200 as cr
+        T, H, D = 8, 2, 128
+        cache = cr.convrot_kv4_new_cache(20, H, 64, D, "cuda")
+        k, q = (torch.randn(T, h, D, device="cuda").bfloat16() for h in (H, 4 * H))
+        x = torch.randn(T, 1024, device="cuda").bfloat16()
+        qw, sg = torch.full((512, 512), 0x21, dtype=torch.uint8, device="cuda"), torch.ones(512, 16, device="cuda").bfloat16()
+        i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+        table, free, count = i32(*[0] * T * 4).view(T, 4), torch.arange(20, device="cuda").int(), i32(20)
+        def step():
+            p = cr.convrot_kv4_plan(i0, i1, table, free, count, 64, T)
+            cr.convrot_kv4_append(k, k, cache, p.slots, 64)
+            return (cr.convrot_kv4_attention(q, cache, table, p.seq_lens, p.cu_q, 0.1, 64),
+                    *cr.convrot_kv4_read(cache, p.slots, 64), cr.convrot_w4g_linear(x, qw, sg, None, 64, 64))
+        i0, i1 = i32(*[0] * T), i32(*[1] * T)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b) and bool(a.float().abs().sum() > 0)
+        print("captured")
+    """
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
 
 
 def test_writes_stay_inside_their_buffers():
