@@ -62,6 +62,16 @@ Tensor empty(at::IntArrayRef size, at::ScalarType dtype, int index) {
     return at::detail::empty_cuda(size, dtype, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
 
+// `count` values at `at` bytes of a buffer, as a tensor of its own (a dispatched
+// view costs as much as an allocation).
+Tensor part(const Tensor &buffer, int64_t at, at::ScalarType dtype, int64_t count) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                        c10::scalarTypeToTypeMeta(dtype));
+    t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(dtype)));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({count});
+    return t;
+}
+
 PyObject *status(convrot_status st) { return PyLong_FromLong(st); }
 
 // A function's body.  Where memory runs out the Python code makes the call
@@ -142,14 +152,20 @@ PyObject *kv4_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (!count) Py_RETURN_NONE;
         const int64_t B = cached->size(0);
         if (fresh->size(0) != B || table->size(0) != B || count->size(0) != 1 || !current(index)) Py_RETURN_NONE;
-        Tensor lens = empty({B}, at::kInt, index), cu_q = empty({B + 1}, at::kInt, index), slots = empty({most}, at::kLong, index),
-               positions = empty({most}, at::kInt, index), result = empty({4}, at::kInt, index);
+        // the results in one buffer, each on 256 bytes
+        auto room = [](int64_t bytes) { return (bytes + 255) & ~int64_t(255); };
+        const int64_t at_cu = room(4 * B), at_slots = at_cu + room(4 * (B + 1)), at_positions = at_slots + room(8 * most),
+                      at_result = at_positions + room(4 * most);
+        const Tensor buffer = empty({at_result + 16}, at::kByte, index);
+        const Tensor lens = part(buffer, 0, at::kInt, B), cu_q = part(buffer, at_cu, at::kInt, B + 1),
+                     slots = part(buffer, at_slots, at::kLong, most), positions = part(buffer, at_positions, at::kInt, most),
+                     result = part(buffer, at_result, at::kInt, 4);
         auto p = [](const Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); };
         const convrot_status st = convrot_kv4_plan(p(*cached), p(*fresh), B, static_cast<int>(page), p(*table), table->size(1),
                                                    p(*pages), pages->size(0), p(*count), most, p(lens), p(cu_q),
                                                    static_cast<int64_t *>(slots.data_ptr()), p(positions), p(result), stream_of(index));
         if (st != CONVROT_OK) return status(st);
-        const Tensor left = result.narrow(0, 0, 1);
+        const Tensor left = part(buffer, at_result, at::kInt, 1);
         return Py_BuildValue("(NNNNNN)", THPVariable_Wrap(lens), THPVariable_Wrap(cu_q), THPVariable_Wrap(slots),
                              THPVariable_Wrap(positions), THPVariable_Wrap(result), THPVariable_Wrap(left));
     });
