@@ -399,12 +399,13 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // Choices, each with both sides measured on the first case, us:
 // - rows of a block (block_rows): 64.5 with 4, 72 with 8, 112 with 16; 8 heads
 //   on a shared one (8 rows): 115 with 4, 72 with 8; 4 queries of 4 heads: 182
-//   with 4, 112 with 8 and 16.  (All of them, and the two last lines, at a time
+//   with 4, 112 with 8 and 16.  (These, and the two lines behind kTurn, at a time
 //   when the first case took 64.5.)
 // - kTurn: 63.0 with 0, 60.6 with 4, 59.6 with 8, 60.6 with 12; the 16 requests
 //   32.9, 27.2, 25.2, 26.8.
 // - outputs_beside: outputs beside the tiles 64.5, in their place 65.2.
 // - four CTAs an SM (128 registers) 64.5, five or six (spills) 70 and 78.
+// - four warps a CTA 58.1, two (and twice the CTAs) 61.7, eight 73.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxCtas = 592;
