@@ -906,10 +906,11 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
                         for (int k = HALF ? 2 : 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
                         mul[x] = 1.0f;
                         if (top > room[nt][x]) {
+                            // of nothing, at first (the room is the column's; l is of
+                            // this lane's keys only, and 0 where all of those underflow)
+                            mul[x] = room[nt][x] == -INFINITY ? 0.0f : ex2(-top);
                             m[nt][x] += top;
                             room[nt][x] = kRoom;
-                            mul[x] = ex2(-top);      // of nothing, at first
-                            if (l[nt][x] == 0.0f) mul[x] = 0.0f;
                             l[nt][x] *= mul[x];
 #pragma unroll
                             for (int blk = 0; blk < NB; ++blk)
