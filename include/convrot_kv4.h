@@ -130,7 +130,10 @@ size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int
  * -2^100 <= scale <= 2^100.  Queries are held as 16-bit whole numbers, off by
  * at most 2^-16 of their row's largest rotated value; rows below 2^-100 count
  * as 0, rows with a NaN or an infinity give NaN, rows of values beyond 2^119
- * may.  Two kernels.
+ * may.  The products of softmax weights and values' scales are rounded to f16
+ * relative to the largest that the query has met among the keys it sees: off by
+ * 2^-11 of each, or by 2^-30 of that largest where they are below 2^-19 of it.
+ * Two kernels.
  */
 convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void *q_bf16,
                                      int64_t ldq, int64_t T, int heads, const int32_t *block_table,

@@ -13,7 +13,7 @@ with d_j = expm1 of what score j may be off (decoding_ref.attention adds that
 up) and E = sum_j p_j d_j for the softmax's sum; (1 + 2^-6) takes their second
 order.  A weight is rounded to f16 (2^-11); one below the f16 range is off by at
 most half a step, 2^-25, where the row's largest weight so far is at least
-2^5 / 2^0.1, so by less than 2^-29 of the largest p_j s_j, times a code of 7, for
+2^6 / 2^0.1, so by less than 2^-29 of the largest p_j s_j, times a code of 7, for
 each of n keys.  The offset of 8 that the codes carry comes and goes in fp32.
 Nothing here depends on a key that the row does not see.
 """
@@ -164,6 +164,84 @@ def test_reference_moves_while_some_keys_underflow(D, G):
         scores[h, j % 8 == h] = -200.0
     scores[:, late] = 9.5
     codes[:, late] = -7
+    check_long(Shaped(scores, scales, codes), G)
+
+
+@pytest.mark.parametrize("D,G", FORMS)
+def test_value_scales_rise_and_fall(D, G):
+    """The values' scales move by 2^24 up and down along the history, the
+    scores against them, so that keys of all scales count."""
+    scores, scales, codes = long_history(D)
+    tile = torch.arange(scores.shape[1]) // 64
+    for h in range(8):
+        wave = 12 * torch.sin(tile / (5.0 + 3 * h))
+        scales[h] *= 2.0 ** wave.round()
+        if h & 1:
+            scores[h] -= wave
+    check_long(Shaped(scores, scales, codes), G)
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 24, 2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("D,G", FORMS)
+def test_a_hidden_value_of_any_scale_changes_nothing(D, G, ratio):
+    """The newest of three tokens has a value far above the others; the two
+    queries before it must not see it."""
+    g = torch.Generator().manual_seed(D + G)
+    for n in (3, 40, 64, 700):
+        codes = torch.randint(-7, 8, (2, n, D), generator=g)
+        scales = (torch.rand(2, n, generator=g) + 0.5) * 0.4
+        scores = torch.randn(2, n, generator=g)
+        scales[:, -1] *= ratio
+        a = Shaped(scores, scales, codes)
+        q = a.queries(3, G)
+        out = a.run(q, 1)
+        for i in range(3):
+            seen = torch.arange(n) <= n - 3 + i
+            for h in range(2):
+                check_rows(out[i, h * G:(h + 1) * G], a.row(q[i, h * G], h, seen), f"n {n}, query {i}, head {h}")
+
+
+@pytest.mark.parametrize("D,G", FORMS)
+@pytest.mark.parametrize("n,where", [(64, 5), (1500, 3), (9000, 70), (9000, 4500)])
+def test_a_large_value_of_no_weight_changes_nothing(D, G, n, where):
+    """A value 2^60 times the others whose softmax weight is 2^-110 of theirs."""
+    scores, scales, codes = long_history(D, n)
+    scores *= 0.5
+    scales[:, where] *= 2.0 ** 60
+    scores[:, where] = -110.0
+    check_long(Shaped(scores, scales, codes), G)
+
+
+@pytest.mark.parametrize("D,G", FORMS)
+@pytest.mark.parametrize("n,where", [(64, 60), (1500, 1400), (9000, 70), (9000, 4500), (9000, 8999)])
+def test_a_small_value_of_all_the_weight_is_the_result(D, G, n, where):
+    """A value 2^-60 times the others, with 2^110 times their softmax weight: it
+    is the result, not what is left of the others."""
+    scores, scales, codes = long_history(D, n)
+    scores *= 0.5
+    scales[:, where] *= 2.0 ** -60
+    scores[:, where] = 110.0
+    check_long(Shaped(scores, scales, codes), G)
+
+
+@pytest.mark.parametrize("D,G", FORMS)
+@pytest.mark.parametrize("n", [50, 9000])
+def test_values_of_zero(D, G, n):
+    """Scales of zero: of the keys that weigh most, and of all of them."""
+    scores, scales, codes = long_history(D, n)
+    scales[:4, ::3] = 0.0
+    scores[:4, ::3] += 30.0
+    scales[4:] = 0.0
+    check_long(Shaped(scores, scales, codes), G)
+
+
+@pytest.mark.parametrize("D,G", FORMS)
+@pytest.mark.parametrize("scale", [2.0 ** -98, 2.0 ** 60])
+def test_values_of_extreme_scales(D, G, scale):
+    """The sums over many keys of the largest and the smallest values."""
+    scores, scales, codes = long_history(D)
+    scales[:] = (scales * scale)
+    codes = codes.abs()
     check_long(Shaped(scores, scales, codes), G)
 
 
