@@ -387,8 +387,8 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // one line, with kTurn more behind each (request, head, row block) for the turn
 // to the next: queries, joining the warps, and warps without a tile.  CTA c takes
 // an even share of the line, so ragged lengths load the GPU evenly and long
-// requests are split.  A CTA whose part ends inside a request writes (max, sum,
-// O) to the workspace and combine_kernel joins the parts in their order.
+// requests are split.  A CTA whose part ends inside a request writes
+// (reference, sum, mean of the values) to the workspace and combine_kernel joins the parts in their order.
 //
 // Measured (CUDA graphs), 64 requests of 1500 to 8192 keys, 32 query heads on 8
 // of 128: 58.0 us for 268 MB, 4.6 TB/s (41.1 us at the copy rate; the copies
@@ -436,7 +436,7 @@ struct AttnArgs {
     int B;
     float scale;             // softmax scale * log2(e)
     int4 *desc;              // per CTA: {last CTA of the request it starts and does not end, b, h, row block}
-    float *parts;            // per CTA two parts: ROWS (max, sum), then ROWS x D
+    float *parts;            // per CTA two parts: ROWS (reference, sum), then ROWS x D
     uint16_t *out;
 };
 
@@ -479,15 +479,19 @@ __device__ __forceinline__ float level_of(uint32_t bits) {
     return fmaf(__uint_as_float((bits & 0x7FFFu) | 0x4B000000u), 1.0f / 128.0f, -65536.0f - 127.0f);
 }
 
+// 1 / the sum of a row's softmax weights, 0 for a row that has none.  Outputs of
+// several warps or CTAs are joined as means by their shares of the sum: a sum
+// of the largest values over many keys would leave fp32.
+__device__ __forceinline__ float share_of(float sum) { return sum > 0.0f || sum != sum ? __fdividef(1.0f, sum) : 0.0f; }
+
 // Output row r of a row block -> rotate back 16 channels a thread and store.
 __device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, int h, int row,
-                                          int part, float (&x)[16], float total) {
+                                          int part, float (&x)[16]) {
     frag::rotate(x, a.c.group == 256);
     const int i = row / a.G;
     if (i < rq.nq) {
-        const float f = total > 0.0f || total != total ? frag::norm_of(a.c.group) / total : 0.0f;
         const int heads = a.G * a.c.heads;
-        frag::store16(a.out + ((static_cast<int64_t>(rq.q0) + i) * heads + h * a.G + row % a.G) * a.c.D + 16 * part, x, f);
+        frag::store16(a.out + ((static_cast<int64_t>(rq.q0) + i) * heads + h * a.G + row % a.G) * a.c.D + 16 * part, x, frag::norm_of(a.c.group));
     }
 }
 
@@ -1086,7 +1090,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
                 if (g == 0) {
                     wm[warp][8 * nt + col0 + x] = room[nt][x] == -INFINITY ? -INFINITY : m[nt][x];
                     wl[warp][8 * nt + col0 + x] = l[nt][x];
-                    wunit[warp][8 * nt + col0 + x] = ex2(limit[nt][x] - kHead - kUnit);
+                    wunit[warp][8 * nt + col0 + x] = limit[nt][x] - kHead - kUnit;
                 }
             }
 #pragma unroll
@@ -1112,9 +1116,11 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             const float safe = top == -INFINITY ? 0.0f : top;
             float x[16] = {}, sum = 0.0f;
 #pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) sum += ex2(wm[w][r] - safe) * wl[w][r];
+            const float share = share_of(sum);
+#pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float e = ex2(wm[w][r] - safe), f = e * wunit[w][r];
-                sum += e * wl[w][r];
+                const float f = ex2(wm[w][r] - safe + wunit[w][r]) * share;
                 const float4 *src = reinterpret_cast<const float4 *>(osum + (w * ROWS + r) * PITCH + 16 * part);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -1126,7 +1132,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
                 }
             }
             if (whole) {
-                store_row(a, rq, h, i < ROWS * LANES ? row0 + r : 0x7FFFFFFF, part, x, sum);
+                store_row(a, rq, h, i < ROWS * LANES ? row0 + r : 0x7FFFFFFF, part, x);
             } else if (i < ROWS * LANES) {
                 if (part == 0) {
                     part_out[2 * r] = top;
@@ -1170,8 +1176,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
     auto at = [&](int k) {   // the k-th part: the first is its CTA's second
         return a.parts + (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * (ROWS * (D + 2));
     };
-    // the group's parts, kBatch on the way at a time, relative to the largest
-    // of the references so far
+    // the mean of the group's parts, kBatch on the way at a time, relative to
+    // the largest of the references so far
     constexpr int kBatch = 2;
     float x[16] = {}, sum = 0.0f, top = -INFINITY;
     if (group < count) {
@@ -1191,14 +1197,19 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
             const float last = top;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u].x);
-            const float safe = top == -INFINITY ? 0.0f : top, f0 = ex2(last - safe);
-            sum *= f0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= f0;
+            const float safe = top == -INFINITY ? 0.0f : top, mine = ex2(last - safe) * sum;
+            sum = mine;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                const float f = ex2(ml[u].x - safe);
-                sum += f * ml[u].y;
+                ml[u].y *= ex2(ml[u].x - safe);
+                sum += ml[u].y;
+            }
+            const float share = share_of(sum);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= mine * share;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float f = ml[u].y * share;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     x[4 * e] += f * y[u][e].x;
@@ -1220,14 +1231,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
     const int groups = min(GROUPS, count);
     float all = top;
     for (int k = 1; k < groups; ++k) all = fmaxf(all, tops[k][i].x);
-    const float safe = all == -INFINITY ? 0.0f : all, f0 = ex2(top - safe);
-    sum *= f0;
+    const float safe = all == -INFINITY ? 0.0f : all, mine = ex2(top - safe) * sum;
+    sum = mine;
+    for (int k = 1; k < groups; ++k) sum += ex2(tops[k][i].x - safe) * tops[k][i].y;
+    const float share = share_of(sum), f0 = mine * share;
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] *= f0;
     for (int k = 1; k < groups; ++k) {
-        const float2 t = tops[k][i];
-        const float f = ex2(t.x - safe);
-        sum += f * t.y;
+        const float f = ex2(tops[k][i].x - safe) * tops[k][i].y * share;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float4 y = sums[k - 1][e][i];
@@ -1237,7 +1248,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
             x[4 * e + 3] += f * y.w;
         }
     }
-    store_row(a, rq, d.z, i < USED ? d.w * ROWS + r : 0x7FFFFFFF, part, x, sum);
+    store_row(a, rq, d.z, i < USED ? d.w * ROWS + r : 0x7FFFFFFF, part, x);
 }
 
 template <int D, int ROWS>

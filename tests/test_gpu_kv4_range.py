@@ -236,7 +236,7 @@ def test_values_of_zero(D, G, n):
 
 
 @pytest.mark.parametrize("D,G", FORMS)
-@pytest.mark.parametrize("scale", [2.0 ** -98, 2.0 ** 60])
+@pytest.mark.parametrize("scale", [2.0 ** -98, 2.0 ** 60, 2.0 ** 118])
 def test_values_of_extreme_scales(D, G, scale):
     """The sums over many keys of the largest and the smallest values."""
     scores, scales, codes = long_history(D)
