@@ -26,7 +26,10 @@
  *
  * Conventions are those of convrot.h (device pointers on the current device,
  * 16-byte aligned, caller-owned buffers, arguments validated before any
- * launch, deterministic results).  A buffer that a call writes overlaps no
+ * launch, deterministic results), but whole-number arrays (slots, lengths,
+ * tables, counts) begin anywhere that their type allows, so that parts of
+ * longer arrays can be given; only the plan's `cached` and `result` begin on 16
+ * bytes.  A buffer that a call writes overlaps no
  * other that it writes or reads (CONVROT_ERR_OVERLAP).  What lies in device
  * memory cannot be validated by the host: a slot or page id outside the cache,
  * where a call reads one, is skipped as if the token were not there, and

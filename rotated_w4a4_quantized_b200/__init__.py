@@ -1169,6 +1169,9 @@ def convrot_kv4_plan(cached, new_tokens, block_table, free_pages, free_count, pa
     if max_tokens < 0:
         raise ValueError("max_tokens is negative")
     i32 = torch.int32
+    if cached.data_ptr() % 16:   # part of a longer array: the C ABI takes these lengths from 16 bytes on
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            cached = cached.clone()
     seq_lens = _empty(B, i32, cached, stream)
     cu_q = _empty(B + 1, i32, cached, stream)
     slots = _empty(max_tokens, torch.int64, cached, stream)

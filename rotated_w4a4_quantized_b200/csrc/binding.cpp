@@ -151,6 +151,7 @@ PyObject *kv4_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const Tensor *count = pages ? dense(args[4], at::kInt, 1, index) : nullptr;
         if (!count) Py_RETURN_NONE;
         const int64_t B = cached->size(0);
+        if (reinterpret_cast<uintptr_t>(cached->data_ptr()) % 16) Py_RETURN_NONE;   // taken as a copy
         if (fresh->size(0) != B || table->size(0) != B || count->size(0) != 1 || !current(index)) Py_RETURN_NONE;
         // the results in one buffer, each on 256 bytes
         auto room = [](int64_t bytes) { return (bytes + 255) & ~int64_t(255); };

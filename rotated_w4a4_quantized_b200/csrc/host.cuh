@@ -59,11 +59,13 @@ convrot_status device_setup(int *dev_out, F kernels) {
     return st.status;
 }
 
-inline bool aligned16(std::initializer_list<const void *> ptrs) {
+inline bool aligned(unsigned bytes, std::initializer_list<const void *> ptrs) {
     for (const void *p : ptrs)
-        if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
+        if (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) return false;
     return true;
 }
+
+inline bool aligned16(std::initializer_list<const void *> ptrs) { return aligned(16, ptrs); }
 
 // CONVROT_OK when every non-null pointer is device (or managed) memory of
 // device `dev`: run before any launch, so a bad pointer never reaches a

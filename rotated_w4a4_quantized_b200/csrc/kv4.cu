@@ -1398,7 +1398,8 @@ convrot_status convrot_kv4_plan(const int32_t *cached, const int32_t *new_tokens
     if (!free_count || !cu_q || !result || (B && (!cached || !new_tokens || !seq_lens || (max_pages && !block_table))) ||
         (capacity && !free_pages) || (max_tokens && (!slots || !positions)))
         return CONVROT_ERR_NULL;
-    if (!host::aligned16({cached, new_tokens, block_table, free_pages, free_count, seq_lens, cu_q, slots, positions, result}))
+    if (!host::aligned16({cached, result}) || !host::aligned(8, {slots}) ||
+        !host::aligned(4, {new_tokens, block_table, free_pages, free_count, seq_lens, cu_q, positions}))
         return CONVROT_ERR_ALIGN;
     int dev;
     convrot_status st = setup(&dev);
@@ -1429,7 +1430,7 @@ convrot_status convrot_kv4_append(const convrot_kv4_cache *cache, const void *k_
     if (T == 0) return CONVROT_OK;
     if (!k_bf16 || !v_bf16 || !slots) return CONVROT_ERR_NULL;
     if ((st = check_cache_ptrs(cache)) != CONVROT_OK) return st;
-    if (!host::aligned16({k_bf16, v_bf16, slots})) return CONVROT_ERR_ALIGN;
+    if (!host::aligned16({k_bf16, v_bf16}) || !host::aligned(8, {slots})) return CONVROT_ERR_ALIGN;
     int dev;
     if ((st = setup(&dev)) != CONVROT_OK) return st;
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
@@ -1459,7 +1460,7 @@ convrot_status convrot_kv4_read(const convrot_kv4_cache *cache, const int64_t *s
     if (T == 0) return CONVROT_OK;
     if (!k_bf16 || !v_bf16 || !slots) return CONVROT_ERR_NULL;
     if ((st = check_cache_ptrs(cache)) != CONVROT_OK) return st;
-    if (!host::aligned16({k_bf16, v_bf16, slots})) return CONVROT_ERR_ALIGN;
+    if (!host::aligned16({k_bf16, v_bf16}) || !host::aligned(8, {slots})) return CONVROT_ERR_ALIGN;
     int dev;
     if ((st = setup(&dev)) != CONVROT_OK) return st;
     if ((st = host::check_device_ptrs(dev, {k_bf16, v_bf16, slots, cache->k_codes, cache->k_scales, cache->v_codes,
@@ -1504,7 +1505,7 @@ convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void 
     if (ws_bytes < need ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return CONVROT_ERR_WORKSPACE;
-    if (!host::aligned16({q_bf16, block_table, seq_lens, cu_q, out_bf16})) return CONVROT_ERR_ALIGN;
+    if (!host::aligned16({q_bf16, out_bf16}) || !host::aligned(4, {block_table, seq_lens, cu_q})) return CONVROT_ERR_ALIGN;
     int dev;
     if ((st = setup(&dev)) != CONVROT_OK) return st;
     if ((st = host::check_device_ptrs(dev, {q_bf16, block_table, seq_lens, cu_q, out_bf16, workspace, cache->k_codes,
