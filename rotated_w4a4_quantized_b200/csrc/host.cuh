@@ -21,7 +21,9 @@ constexpr int kMaxDevices = 64;
 
 // `ready` is stored (release) only after every other field is written and
 // read (acquire) before any of them; the first set-up on each device runs
-// under the lock.
+// under the lock.  A CUDA call that failed (for want of memory while the
+// kernels load, say) is tried again by the next call: only what cannot change,
+// success and another kind of device, is kept.
 struct DeviceState {
     std::atomic<bool> ready{false};
     convrot_status status = CONVROT_OK;
@@ -54,6 +56,10 @@ convrot_status device_setup(int *dev_out, F kernels) {
         st.status = CONVROT_ERR_UNSUPPORTED;
     else
         st.status = kernels() ? CONVROT_OK : CONVROT_ERR_CUDA;
+    if (st.status == CONVROT_ERR_CUDA) {
+        cudaGetLastError();   // reported here: no later launch finds it
+        return st.status;
+    }
     st.num_sms = sms;
     st.ready.store(true, std::memory_order_release);
     return st.status;
@@ -122,7 +128,9 @@ convrot_status launch_dependent(K *kernel, dim3 grid, dim3 block, size_t smem, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return CONVROT_OK;
+    cudaGetLastError();       // as above
+    return CONVROT_ERR_CUDA;
 }
 
 }  // namespace

@@ -1371,8 +1371,10 @@ template <int D, int ROWS>
 convrot_status launch_attention(AttnArgs a, int64_t ctas, int sms, cudaStream_t stream) {
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_kernel<D, ROWS>, kAttnThreads,
-                                                      attn_smem<D, ROWS>()) != cudaSuccess)
+                                                      attn_smem<D, ROWS>()) != cudaSuccess) {
+        cudaGetLastError();
         return CONVROT_ERR_CUDA;
+    }
     if (ctas > static_cast<int64_t>(sms) * per_sm) ctas = static_cast<int64_t>(sms) * per_sm;
     const dim3 grid(static_cast<unsigned>(ctas));
     if (host::launch_dependent(attention_kernel<D, ROWS>, grid, dim3(kAttnThreads), attn_smem<D, ROWS>(), stream, a) != CONVROT_OK)
