@@ -918,7 +918,7 @@ def _native():
         try:
             from . import _decoding
         except ImportError as e:
-            raise RuntimeError("the extension module _decoding is missing: build it with "
+            raise RuntimeError("the extension module _decoding is missing or does not fit this torch: build it with "
                                "`python -m rotated_w4a4_quantized_b200.build` (there is no fallback path)") from e
         _extension = _decoding
     return _extension

@@ -73,10 +73,24 @@ def _stale(lib: str, deps) -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _built_against() -> str:
+    """What the extension module's machine code depends on beside its sources:
+    it is compiled against torch's C++ interfaces, which change with torch."""
+    import torch
+    return f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sys.version.split()[0]}"
+
+
+def _binding_stale() -> bool:
+    if _stale(LIB_BINDING, DEPS_BINDING) or not os.path.exists(LIB_BINDING + ".built"):
+        return True
+    with open(LIB_BINDING + ".built") as f:
+        return f.read() != _built_against()
+
+
 def stale() -> bool:
     return (_stale(LIB, DEPS + [HEADER]) or _stale(LIB_W4A16, DEPS_W4A16)
             or _stale(LIB_NVFP4, DEPS_NVFP4) or _stale(LIB_W4G, DEPS_W4G)
-            or _stale(LIB_KV4, DEPS_KV4) or _stale(LIB_BINDING, DEPS_BINDING))
+            or _stale(LIB_KV4, DEPS_KV4) or _binding_stale())
 
 
 def _build_one(src: str, lib: str, verbose: bool) -> None:
@@ -105,11 +119,15 @@ def _build_binding(verbose: bool) -> None:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_BINDING)
+    with open(tmp, "w") as f:
+        f.write(_built_against())
+    os.replace(tmp, LIB_BINDING + ".built")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build whichever library is missing or older than its sources; returns
-    the W4A4 library's path."""
+    """Build whichever library is missing or older than its sources, and the
+    extension module also where it was built against another torch or Python;
+    returns the W4A4 library's path."""
     if force or _stale(LIB, DEPS + [HEADER]):
         _build_one(SRC, LIB, verbose)
     if force or _stale(LIB_W4A16, DEPS_W4A16):
@@ -120,7 +138,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         _build_one(SRC_W4G, LIB_W4G, verbose)
     if force or _stale(LIB_KV4, DEPS_KV4):
         _build_one(SRC_KV4, LIB_KV4, verbose)
-    if force or _stale(LIB_BINDING, DEPS_BINDING):
+    if force or _binding_stale():
         _build_binding(verbose)
     return LIB
 
