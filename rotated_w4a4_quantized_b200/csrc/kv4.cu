@@ -388,7 +388,7 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // to the next: queries, joining the warps, and warps without a tile.  CTA c takes
 // an even share of the line, so ragged lengths load the GPU evenly and long
 // requests are split.  A CTA whose part ends inside a request writes
-// (reference, sum, mean of the values) to the workspace and combine_kernel joins the parts in their order.
+// (log2 of the softmax's sum, mean of the values) to the workspace and combine_kernel joins the parts in their order.
 //
 // Measured (CUDA graphs), 64 requests of 1500 to 8192 keys, 32 query heads on 8
 // of 128: 58.0 us for 268 MB, 4.6 TB/s (41.1 us at the copy rate; the copies
@@ -436,7 +436,7 @@ struct AttnArgs {
     int B;
     float scale;             // softmax scale * log2(e)
     int4 *desc;              // per CTA: {last CTA of the request it starts and does not end, b, h, row block}
-    float *parts;            // per CTA two parts: ROWS (reference, sum), then ROWS x D
+    float *parts;            // per CTA two parts: ROWS (log2 of the softmax's sum, -), then ROWS x D
     uint16_t *out;
 };
 
@@ -479,10 +479,17 @@ __device__ __forceinline__ float level_of(uint32_t bits) {
     return fmaf(__uint_as_float((bits & 0x7FFFu) | 0x4B000000u), 1.0f / 128.0f, -65536.0f - 127.0f);
 }
 
-// 1 / the sum of a row's softmax weights, 0 for a row that has none.  Outputs of
-// several warps or CTAs are joined as means by their shares of the sum: a sum
-// of the largest values over many keys would leave fp32.
-__device__ __forceinline__ float share_of(float sum) { return sum > 0.0f || sum != sum ? __fdividef(1.0f, sum) : 0.0f; }
+// log2 of the sum of a row's softmax weights; 0 for a row that has none.
+// Outputs of several warps or CTAs are joined as means by their shares of the
+// sum: a sum of the largest values over many keys would leave fp32.  (The sum's
+// rounding as a logarithm, 2^-24 of it, is below that of the scores' own fp32
+// products.  With reference and sum apart, and a division a step: 58.3 us
+// against 57.5.)
+__device__ __forceinline__ float log_of(float sum) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sum));
+    return sum > 0.0f || sum != sum ? r : 0.0f;
+}
 
 // Output row r of a row block -> rotate back 16 channels a thread and store.
 __device__ __forceinline__ void store_row(const AttnArgs &a, const Request &rq, int h, int row,
@@ -1117,10 +1124,10 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             float x[16] = {}, sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) sum += ex2(wm[w][r] - safe) * wl[w][r];
-            const float share = share_of(sum);
+            const float log = log_of(sum);
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = ex2(wm[w][r] - safe + wunit[w][r]) * share;
+                const float f = ex2(wm[w][r] - safe + (wunit[w][r] - log));
                 const float4 *src = reinterpret_cast<const float4 *>(osum + (w * ROWS + r) * PITCH + 16 * part);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -1134,10 +1141,7 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             if (whole) {
                 store_row(a, rq, h, i < ROWS * LANES ? row0 + r : 0x7FFFFFFF, part, x);
             } else if (i < ROWS * LANES) {
-                if (part == 0) {
-                    part_out[2 * r] = top;
-                    part_out[2 * r + 1] = sum;
-                }
+                if (part == 0) part_out[2 * r] = top + log;
                 float4 *dst = reinterpret_cast<float4 *>(part_out + 2 * ROWS + r * D + 16 * part);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
@@ -1178,38 +1182,36 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
     };
     // the mean of the group's parts, kBatch on the way at a time, relative to
     // the largest of the references so far
+    // (kShare: all parts of a grid together stay below the largest of their means)
     constexpr int kBatch = 2;
+    constexpr float kShare = 1.0f / 1024.0f;
+    static_assert(kMaxCtas < 1024);
     float x[16] = {}, sum = 0.0f, top = -INFINITY;
     if (group < count) {
 #pragma unroll 1
         for (int k0 = group; k0 < count; k0 += kBatch * GROUPS) {
-            float2 ml[kBatch];
+            float log[kBatch];
             float4 y[kBatch][4];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int k = k0 + u * GROUPS;
                 const float *p = at(min(k, count - 1));
                 const float4 *src = reinterpret_cast<const float4 *>(p + 2 * ROWS + r * D + 16 * part);
-                ml[u] = k < count ? *reinterpret_cast<const float2 *>(p + 2 * r) : make_float2(-INFINITY, 0.0f);
+                log[u] = k < count ? p[2 * r] : -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[u][e] = k < count ? src[e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             const float last = top;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u].x);
-            const float safe = top == -INFINITY ? 0.0f : top, mine = ex2(last - safe) * sum;
-            sum = mine;
+            for (int u = 0; u < kBatch; ++u) top = fmaxf(top, log[u]);
+            const float safe = top == -INFINITY ? 0.0f : top, f0 = ex2(last - safe);
+            sum *= f0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= f0;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                ml[u].y *= ex2(ml[u].x - safe);
-                sum += ml[u].y;
-            }
-            const float share = share_of(sum);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= mine * share;
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const float f = ml[u].y * share;
+                const float f = kShare * ex2(log[u] - safe);
+                sum += f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     x[4 * e] += f * y[u][e].x;
@@ -1231,14 +1233,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
     const int groups = min(GROUPS, count);
     float all = top;
     for (int k = 1; k < groups; ++k) all = fmaxf(all, tops[k][i].x);
-    const float safe = all == -INFINITY ? 0.0f : all, mine = ex2(top - safe) * sum;
-    sum = mine;
-    for (int k = 1; k < groups; ++k) sum += ex2(tops[k][i].x - safe) * tops[k][i].y;
-    const float share = share_of(sum), f0 = mine * share;
+    const float safe = all == -INFINITY ? 0.0f : all, f0 = ex2(top - safe);
+    sum *= f0;
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] *= f0;
     for (int k = 1; k < groups; ++k) {
-        const float f = ex2(tops[k][i].x - safe) * tops[k][i].y * share;
+        const float2 t = tops[k][i];
+        const float f = ex2(t.x - safe);
+        sum += f * t.y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float4 y = sums[k - 1][e][i];
@@ -1248,6 +1250,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a) {
             x[4 * e + 3] += f * y.w;
         }
     }
+    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] *= f;
     store_row(a, rq, d.z, i < USED ? d.w * ROWS + r : 0x7FFFFFFF, part, x);
 }
 
