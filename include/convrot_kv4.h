@@ -136,7 +136,9 @@ size_t convrot_kv4_attention_workspace_size(int64_t T, int64_t B, int heads, int
  * may.  The products of softmax weights and values' scales are rounded to f16
  * relative to the largest that the query has met among the keys it sees: off by
  * 2^-11 of each, or by 2^-30 of that largest where they are below 2^-19 of it.
- * Two kernels.
+ * Softmax weights below 2^-110 of the query's largest may count as 0, and scores
+ * have to stay in fp32's range.  Lengths and queries beyond what block_table and
+ * q_bf16 hold are cut.  Two kernels.
  */
 convrot_status convrot_kv4_attention(const convrot_kv4_cache *cache, const void *q_bf16,
                                      int64_t ldq, int64_t T, int heads, const int32_t *block_table,

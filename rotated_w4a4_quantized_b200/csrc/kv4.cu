@@ -377,8 +377,8 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // 16-byte asynchronous copies: no warp waits for another inside a request.
 // (Bulk copies take 25 instructions each, a lane at a time: 80 us against 68.)
 // The 8 lanes that copy a block of 16 keys look its page up, so that pages of
-// any size cost the same (pages of 16: 63.2 us, against 74.6 with a lane's copies
-// spread over the blocks).  The next tile's keys are requested as soon as this
+// any size cost nearly the same (pages of 16: 58.9 us, of 64: 57.5; with a lane's
+// copies spread over the blocks pages of 16 took 74.6 where this took 63.2).  The next tile's keys are requested as soon as this
 // one's scores are there, its values after the second product: with 16 warps an
 // SM a warp has several times the copy's latency until it needs them, and
 // registers, not bytes on the way, are what is short.
@@ -391,24 +391,23 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // (log2 of the softmax's sum, mean of the values) to the workspace and combine_kernel joins the parts in their order.
 //
 // Measured (CUDA graphs), 64 requests of 1500 to 8192 keys, 32 query heads on 8
-// of 128: 58.0 us for 268 MB, 4.6 TB/s (41.1 us at the copy rate; the copies
+// of 128: 57.5 us for 268 MB, 4.7 TB/s (41.1 us at the copy rate; the copies
 // alone, without arithmetic, took 63.7 us when all of it took 65).  A steady loop of the same copies
 // reads 6.1 TB/s; what is missing is the start (6.4 us to the first keys: launch,
 // prefix of the lengths, table, latency), uneven ends (CTAs end 7 us after the
 // mean) and the joining kernel (4 us).  2 requests of up to 131072 keys, 64 heads
-// on 8: 56.9 us, 4.3 TB/s.  16 requests of up to 3001 keys, 5 queries, 16 heads
-// on 4 of 256: 25.5 us, latency of few tiles a warp.
+// on 8: 57.6 us, 4.2 TB/s.  16 requests of up to 3001 keys, 5 queries, 16 heads
+// on 4 of 256: 24.8 us, latency of few tiles a warp.
 //
 // Choices, each with both sides measured on the first case, us:
-// - rows of a block (block_rows): 64.5 with 4, 72 with 8, 112 with 16; 8 heads
-//   on a shared one (8 rows): 115 with 4, 72 with 8; 4 queries of 4 heads: 182
-//   with 4, 112 with 8 and 16.  (These, and the two lines behind kTurn, at a time
-//   when the first case took 64.5.)
-// - kTurn: 63.0 with 0, 60.6 with 4, 59.6 with 8, 60.6 with 12; the 16 requests
-//   32.9, 27.2, 25.2, 26.8.
-// - outputs_beside: outputs beside the tiles 64.5, in their place 65.2.
-// - four CTAs an SM (128 registers) 64.5, five or six (spills) 70 and 78.
-// - four warps a CTA 58.1, two (and twice the CTAs) 61.7, eight 73.
+// - rows of a block (block_rows): 57.4 with 4, 63.0 with 8, 92.6 with 16; 8 heads
+//   on a shared one (8 rows): 99 with 4, 63.0 with 8; 4 queries of 4 heads: 158
+//   with 4, 97.6 with 8, 93.1 with 16.
+// - kTurn: 60.3 with 0, 58.3 with 4, 57.4 with 8, 58.1 with 12; the 16 requests
+//   32.3, 26.3, 24.8, 26.2.
+// - outputs_beside: outputs beside the tiles 57.4, in their place 58.0.
+// - four CTAs an SM (128 registers) 57.4, five or six (spills) 65 and 70.
+// - four warps a CTA 57.4, two (and twice the CTAs) 59.1, eight 74.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxCtas = 592;
@@ -1162,8 +1161,8 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
 // Bound by latency (about 4 us behind the attention; a launch of its own costs
 // less than a count of arrivals and the last CTA joining: 69 and 74 us for the
 // two long cases).  256 threads with 64 registers fit into the place of one
-// attention CTA that has ended: two parts on the way a thread give 59.4 us, four
-// (76 registers) 60.8, 512 threads 66.9.
+// attention CTA that has ended: two parts on the way a thread give 57.4 us, four
+// 58.2, 512 threads 59.7.
 constexpr int kCombineThreads = 256;
 
 template <int D, int ROWS>

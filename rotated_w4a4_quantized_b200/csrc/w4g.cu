@@ -154,16 +154,18 @@ prepare_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int group, int 
 //
 // Choices, each with both sides measured on the first layer, us:
 // - columns (TOK 4, 8, 16: the smallest that holds the tokens).  One token
-//   10.5 with 4, 11.4 with 8, 14.1 with 16; 8 tokens 13.0 with 8, 15.9 with 16.
+//   10.1 with 4, 11.2 with 8, 14.0 with 16; 8 tokens 12.8 with 8, 15.8 with 16.
 // - the rows' numbers.  Few rows are turned into numbers by every CTA while its
 //   first weights are on their way, more by prepare_kernel once.  Two tokens
-//   11.2 in the product, 12.3 with prepare_kernel; 5 tokens 14.1 and 12.5.  They
-//   meet at kFusedLanes (4 tokens: 12.7 and 12.4; 1024 -> 4096, 8 tokens: 4.3
-//   and 5.0).
+//   10.6 in the product, 12.0 with prepare_kernel; 5 tokens 14.0 and 12.4.  They
+//   meet at kFusedLanes (4 tokens: 12.1 and 12.3; 1024 -> 4096, 8 tokens: 4.2
+//   and 4.9).
 // - stages of a ring (depth_of): one on its way while one is used is enough
-//   for 16 warps, and more only delay the activations' loads.  One token 10.3
-//   with 2, 10.4 with 3, 10.7 with 4; 16 tokens 15.0, 15.6, 15.6.  But 5 tokens
-//   with scale groups of 32 take 13.7 with 2 and 12.6 with 3.
+//   for 16 warps, and more only delay the activations' loads.  Measured for 1,
+//   4, 5, 8, 9 and 16 tokens, scale groups of 32, 64 and 128, and 1024 -> 4096,
+//   4096 -> 14336, 12288 -> 8197: 5 and 8 tokens with groups of 32 take 0.5, 9
+//   and 4% less with 3 stages than with 2 (4096 -> 14336, 5 tokens: 12.6 against
+//   13.9); every other class takes between 1% less and 6% more.
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStageBytes = 16 * kStage / 2;
