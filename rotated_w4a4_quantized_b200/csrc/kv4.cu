@@ -378,17 +378,19 @@ read_kernel(Cache c, const long long *__restrict__ slots, I total, uint16_t *__r
 // (Bulk copies take 25 instructions each, a lane at a time: 80 us against 68.)
 // The 8 lanes that copy a block of 16 keys look its page up, so that pages of
 // any size cost nearly the same (pages of 16: 58.9 us, of 64: 57.5; with a lane's
-// copies spread over the blocks pages of 16 took 74.6 where this took 63.2).  The next tile's keys are requested as soon as this
-// one's scores are there, its values after the second product: with 16 warps an
-// SM a warp has several times the copy's latency until it needs them, and
-// registers, not bytes on the way, are what is short.
+// copies spread over the blocks pages of 16 took 74.6 where this took 63.2).
+// The next tile's keys are requested as soon as this one's scores are there, its
+// values after the second product: with 16 warps an SM a warp has several times
+// the copy's latency until it needs them, and registers, not bytes on the way,
+// are what is short.
 //
 // Work.  Units of one tile for one (request, head, row block) are laid out in
 // one line, with kTurn more behind each (request, head, row block) for the turn
 // to the next: queries, joining the warps, and warps without a tile.  CTA c takes
 // an even share of the line, so ragged lengths load the GPU evenly and long
-// requests are split.  A CTA whose part ends inside a request writes
-// (log2 of the softmax's sum, mean of the values) to the workspace and combine_kernel joins the parts in their order.
+// requests are split.  A CTA whose part ends inside a request writes (log2 of the
+// softmax's sum, mean of the values) to the workspace and combine_kernel joins
+// the parts in their order.
 //
 // Measured (CUDA graphs), 64 requests of 1500 to 8192 keys, 32 query heads on 8
 // of 128: 57.5 us for 268 MB, 4.7 TB/s (41.1 us at the copy rate; the copies
@@ -891,14 +893,15 @@ __global__ void __launch_bounds__(kAttnThreads, D > 128 || ROWS > 8 ? 2 : ROWS =
             __syncwarp();
             // ---- does a score or a weight leave its reference's room?  Hidden
             // keys' are -inf.  For the weights a lane takes its largest score with
-            // its largest scale first, which is no less than its largest weight.
+            // its largest scale first, which is no less than its largest weight
+            // (without signs: hidden keys' scales are whatever memory held).
             uint32_t scale_bits[NB][NS / 2], wide = 0;
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
                 for (int y = 0; y < NS / 2; ++y) {
                     scale_bits[blk][y] = svs[16 * blk + key0 + 8 * y];
-                    wide = max(wide, scale_bits[blk][y]);
+                    wide = max(wide, scale_bits[blk][y] & 0x7FFFu);
                 }
             const float widest = level_of(wide);
             // the largest of f(a score, its key's scale) of this lane's keys in a column

@@ -275,3 +275,18 @@ def test_a_prompt_among_long_histories(D, G):
             continue
         for h in range(2):
             check_rows(out[row, h * G:(h + 1) * G], a.row(q[0, 0], h, j <= lens[b] - new[b] + i), f"request {b}, query {i}")
+
+
+@pytest.mark.parametrize("left", [-2.0 ** -100, -1.0, float("nan"), float("-inf"), 1e38])
+@pytest.mark.parametrize("D,G", FORMS)
+def test_what_lies_behind_the_end_hides_no_larger_scale(D, G, left):
+    """The scales of the last tile's values are far above all before them; beside
+    them, behind the request's end, lies whatever the memory held."""
+    scores, scales, codes = long_history(D)
+    n = scores.shape[1]
+    assert n % 64 == 40
+    scales[:, n - 40:] *= 2.0 ** 14
+    a = Shaped(scores, scales, codes)
+    a.cache.v_scales[a.order[-1], :, n % PAGE:] = left
+    a.cache.k_scales[a.order[-1], :, n % PAGE:] = left
+    check_long(a, G)
